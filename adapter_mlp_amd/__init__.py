@@ -22,6 +22,7 @@ __all__ = [
     "mlp_fwd", "mlp_bwd", "mlp_workspace_size",
     "relu2_mlp_fwd", "relu2_mlp_bwd", "relu2_mlp_workspace_size",
     "qkv_fwd", "qkv_bwd", "o_fwd", "o_bwd", "o_fwd_noalloc",
+    "block_norm_fwd", "block_norm_bwd", "block_norm_workspace_size",
     "nf4_quantize", "nf4_dequant", "nf4_unpack_codes", "nf4_gemm", "nf4_codebook",
     "trace_begin", "trace_end",
 ]
@@ -582,6 +583,130 @@ def o_bwd(dY, X, U, o: Proj, *, dX=None, dA=None, dB=None, ws=None, stream=None,
     L.call("lora_o_bwd", C.byref(d), _ptr(dY), _ptr(X), _ptr(U), C.byref(o.c_struct(keep)), _ptr(dX), _ptr(dA),
            _ptr(dB), _ptr(ws), _nbytes(ws, X.device), _stream(stream))
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block
+# ---------------------------------------------------------------------------
+
+def _call_on(t, stream, name, *args):
+    """L.call(name, *args, stream) on t's device, with the given stream or that
+    device's current one."""
+    torch = _torch()
+    dev = t.device
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    if torch.cuda.current_device() == dev.index:
+        L.call(name, *args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            L.call(name, *args, stream.cuda_stream)
+
+
+def _norm_call(R, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset):
+    """The checked descriptor of a block norm over rows like R's."""
+    torch = _torch()
+    T, H = _x2d("R", R)
+    dt = _dtype_code(R)
+    _need("R", R, (T, H), R.dtype, R.device)
+    if Y is not None:
+        _need("Y", Y, (T, H), R.dtype, R.device)
+    kind = L.LORA_GATE_NONE
+    if gate is not None:
+        shape = tuple(gate.shape)
+        kind = (L.LORA_GATE_COL if shape == (H,) else L.LORA_GATE_ROW if shape == (T, 1)
+                else L.LORA_GATE_ELEM if shape == (T, H) else None)
+        if kind is None:
+            raise ValueError(f"gate has shape {shape}, expected ({H},), ({T}, 1) or ({T}, {H})")
+    params = [(n, p) for n, p in (("w_pre", w_pre), ("w_post", w_post), ("gate", gate if kind == L.LORA_GATE_COL else None))
+              if p is not None]
+    pd = params[0][1].dtype if params else R.dtype
+    if pd != R.dtype:
+        if R.dtype != torch.bfloat16 or pd != torch.float32:
+            raise ValueError(f"parameters in {pd} with activations in {R.dtype} are not supported")
+        dt = L.LORA_BF16_F32LORA
+    for n, p in params:
+        _need(n, p, (H,), pd, R.device)
+    if kind in (L.LORA_GATE_ROW, L.LORA_GATE_ELEM):
+        _need("gate", gate, gate.shape, R.dtype, R.device)
+    return L.lora_norm_desc(T, H, eps, res_scale, branch_scale, int(unit_offset), kind, dt, 0)
+
+
+def block_norm_workspace_size(T, H, dtype=L.LORA_BF16):
+    """Bytes of the backward's workspace (the forward takes none)."""
+    d = L.lora_norm_desc(T, H, 0.0, 1.0, 1.0, 0, L.LORA_GATE_NONE, dtype, 0)
+    b = C.c_size_t()
+    L.call("lora_block_norm_workspace_size", C.byref(d), C.byref(b))
+    return b.value
+
+
+def block_norm_fwd(R, Y=None, *, w_pre=None, w_post=None, gate=None, res_scale=1.0, branch_scale=1.0, eps=1e-6,
+                   unit_offset=False, R_out=None, X=None, stream=None):
+    """Residual, gate and norms around a block with residual R and output Y, both [T, H]:
+
+        p = norm(Y) w_post   (Y itself without w_post)
+        R_out = res_scale R + branch_scale gate p
+        X = norm(R_out) w_pre
+
+    norm(v) = v / sqrt(mean(v^2) + eps) per row; unit_offset multiplies by 1 + w instead of w.
+    gate: one value per column [H], per row [T, 1] or per element [T, H].
+    Returns (R_out, X): X is None without w_pre; without Y (the first norm of a model) X = norm(R) w_pre and
+    R_out is R.  R_out=R adds in place."""
+    torch = _torch()
+    d = _norm_call(R, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset)
+    if Y is None and R_out is not None and R_out is not R:
+        raise ValueError("R_out is written only when Y is given")
+    if w_pre is None and X is not None:
+        raise ValueError("X is written only when w_pre is given")
+    if Y is not None and R_out is not None:
+        _need("R_out", R_out, R.shape, R.dtype, R.device)
+    if X is not None:
+        _need("X", X, R.shape, R.dtype, R.device)
+    _on_gpu(R)
+    with _on(stream):
+        if Y is not None and R_out is None:
+            R_out = torch.empty_like(R)
+        if w_pre is not None and X is None:
+            X = torch.empty_like(R)
+    _call_on(R, stream, "lora_block_norm_fwd", C.byref(d), _ptr(R), _ptr(Y), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+             None if Y is None else _ptr(R_out), _ptr(X))
+    return (R if Y is None else R_out), X
+
+
+def block_norm_bwd(dR_out, dX, R_out, Y=None, *, w_pre=None, w_post=None, gate=None, res_scale=1.0, branch_scale=1.0,
+                   eps=1e-6, unit_offset=False, dR=None, dY=None, grads=None, ws=None, stream=None):
+    """Gradients of block_norm_fwd, from those of its outputs (dR_out may be None: zero; dX exactly when the
+    forward had w_pre), its R_out and its Y.  Returns (dR, dY, grads): grads holds "w_pre", "w_post" and "gate"
+    for those the forward had, each of its parameter's shape and dtype; dY is None without Y.  dR and dY may be
+    given, and may be dR_out, dX, R_out or Y themselves."""
+    torch = _torch()
+    d = _norm_call(R_out, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset)
+    for name, t, wanted in (("dR_out", dR_out, False), ("dX", dX, w_pre is not None), ("dR", dR, False), ("dY", dY, False)):
+        if t is not None or wanted:
+            _need(name, t, R_out.shape, R_out.dtype, R_out.device)
+    if dX is not None and w_pre is None:
+        raise ValueError("dX needs w_pre")
+    if dY is not None and Y is None:
+        raise ValueError("dY needs Y")
+    params = {k: p for k, p in (("w_pre", w_pre), ("w_post", w_post), ("gate", gate)) if p is not None}
+    if grads is not None:
+        for k, p in params.items():
+            _need(f"grads[{k!r}]", grads.get(k), p.shape, p.dtype, R_out.device)
+    _on_gpu(R_out, ws)
+    with _on(stream):
+        dR = torch.empty_like(R_out) if dR is None else dR
+        if Y is not None and dY is None:
+            dY = torch.empty_like(Y)
+        if grads is None:
+            grads = {k: torch.empty_like(p) for k, p in params.items()}
+        if ws is None:
+            ws = _ws(block_norm_workspace_size(d.T, d.H, d.dtype), R_out.device)
+    gr = L.lora_norm_grads(*(_ptr(grads.get(k)) if k in params else None for k in ("gate", "w_post", "w_pre")))
+    _call_on(R_out, stream, "lora_block_norm_bwd", C.byref(d), _ptr(dR_out), _ptr(dX), _ptr(R_out), _ptr(Y), _ptr(gate),
+             _ptr(w_post), _ptr(w_pre), _ptr(dR), _ptr(dY), C.byref(gr), _ptr(ws), _nbytes(ws, R_out.device))
+    return dR, dY, grads
 
 
 # ---------------------------------------------------------------------------

@@ -14,6 +14,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "liblora_mi3
 LORA_OK, LORA_EINVAL, LORA_ESHAPE, LORA_EDTYPE, LORA_EALIGN, LORA_EWORKSPACE, LORA_EUNSUPPORTED, LORA_EDEVICE = range(8)
 LORA_F32, LORA_BF16, LORA_BF16_F32LORA = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 32 << 20  # LORA_NOALLOC_SCRATCH_BYTES
+LORA_GATE_NONE, LORA_GATE_COL, LORA_GATE_ROW, LORA_GATE_ELEM = range(4)
 LORA_ACT_SWIGLU, LORA_ACT_GEGLU_TANH = 0, 1
 ACT_CODES = {"swiglu": LORA_ACT_SWIGLU, "geglu_tanh": LORA_ACT_GEGLU_TANH}
 STATUS_NAMES = {0: "LORA_OK", 1: "LORA_EINVAL", 2: "LORA_ESHAPE", 3: "LORA_EDTYPE", 4: "LORA_EALIGN",
@@ -85,6 +86,15 @@ class lora_o_desc(C.Structure):
                 ("plan", C.POINTER(lora_plan))]
 
 
+class lora_norm_desc(C.Structure):
+    _fields_ = [("T", i64), ("H", i64), ("eps", C.c_float), ("res_scale", C.c_float), ("branch_scale", C.c_float),
+                ("unit_offset", i32), ("gate", i32), ("dtype", i32), ("reserved", i32)]
+
+
+class lora_norm_grads(C.Structure):
+    _fields_ = [("dgate", vp), ("dw_post", vp), ("dw_pre", vp)]
+
+
 P = C.POINTER
 SIGNATURES = {
     "lora_version": (i32, []),
@@ -110,6 +120,9 @@ SIGNATURES = {
     "lora_o_fwd": (i32, [P(lora_o_desc), vp, P(lora_proj), vp, vp, vp, sz, vp]),
     "lora_o_bwd": (i32, [P(lora_o_desc), vp, vp, vp, P(lora_proj), vp, vp, vp, vp, sz, vp]),
     "lora_o_fwd_noalloc": (i32, [P(lora_o_desc), vp, P(lora_proj), vp, vp, vp]),
+    "lora_block_norm_workspace_size": (i32, [P(lora_norm_desc), P(sz)]),
+    "lora_block_norm_fwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp]),
+    "lora_block_norm_bwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp, P(lora_norm_grads), vp, sz, vp]),
     "lora_nf4_quantize_workspace_size": (i32, [i64, i64, P(sz)]),
     "lora_nf4_quantize": (i32, [vp, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp]),
     "lora_nf4_dequant": (i32, [P(lora_nf4), vp, i32, vp]),

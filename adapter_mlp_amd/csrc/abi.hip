@@ -10,6 +10,7 @@
 #include <mutex>
 #include <string>
 
+#include "abi.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 #include "trace.hpp"
@@ -24,8 +25,9 @@ namespace {
 
 thread_local std::string g_last_error = "no error";
 
-lora_status fail(lora_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
-lora_status fail(lora_status s, const char* fmt, ...) {
+}  // namespace
+
+lora_status lora::fail(lora_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -35,26 +37,9 @@ lora_status fail(lora_status s, const char* fmt, ...) {
   return s;
 }
 
-#define CHECK(cond, status, ...)          \
-  do {                                    \
-    if (!(cond)) return fail(status, __VA_ARGS__); \
-  } while (0)
-
-#define LAUNCH(expr)                                                              \
-  do {                                                                            \
-    hipError_t e_ = (expr);                                                       \
-    if (e_ != hipSuccess) return fail(LORA_EDEVICE, "%s: %s", #expr, hipGetErrorString(e_)); \
-  } while (0)
-
-// LAUNCH with the launch bracketed for lora_trace_* under `name`.
-#define LAUNCHN(name, stream, expr)       \
-  do {                                    \
-    TraceScope ts_(name, stream);         \
-    LAUNCH(expr);                         \
-  } while (0)
+namespace {
 
 inline int64_t pad16(int64_t x) { return (x + 15) / 16 * 16; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 struct Ctx {
   bool bf16;
@@ -64,21 +49,6 @@ struct Ctx {
   // Width of the GEMM's LoRA K tile: one full 64-wide tile (zero-padded) in bf16.
   int64_t rl(int64_t w) const { return bf16 ? 64 : w; }
 };
-
-// Bump allocator over the caller's workspace (256-byte aligned pieces).
-struct Ws {
-  char* base;
-  size_t off = 0;
-  explicit Ws(void* b) : base(static_cast<char*>(b)) {}
-  void* take(size_t bytes) {
-    off = (off + 255) & ~(size_t)255;
-    void* p = base ? base + off : nullptr;
-    off += bytes;
-    return p;
-  }
-};
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // `adapters` admits LORA_BF16_F32LORA (the calls that take adapters).
 lora_status check_dtype(int32_t dtype, Ctx& c, bool adapters = false) {
@@ -125,12 +95,6 @@ lora_status check_tptr(const Ctx& c, const void* p, int64_t T, const char* name)
   return check_ptr(c, p, name);
 }
 
-#define TRY(expr)                    \
-  do {                               \
-    lora_status s_ = (expr);         \
-    if (s_ != LORA_OK) return s_;    \
-  } while (0)
-
 lora_status check_nf4(const lora_nf4* q, int64_t rows, int64_t cols, const char* name) {
   CHECK(q->codes && q->q8 && q->s2 && q->mu, LORA_EINVAL, "%s: NF4 array pointer is NULL", name);
   CHECK(q->rows == rows && q->cols == cols, LORA_ESHAPE,
@@ -160,12 +124,6 @@ lora_status check_proj(const Ctx& c, const lora_proj* p, int64_t n_in, int64_t n
   TRY(check_ptr(c, p->B, name));
   CHECK(std::isfinite(p->scale), LORA_EINVAL, "%s: scale is not finite", name);
   return LORA_OK;
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const char* x = static_cast<const char*>(a);
-  const char* y = static_cast<const char*>(b);
-  return x < y + nb && y < x + na;
 }
 
 BSrc bsrc(const lora_proj* p, int64_t ld) {
@@ -413,13 +371,6 @@ struct PackBatch {
     add(a);
   }
 };
-
-lora_status check_ws(const void* ws, size_t have, size_t need) {
-  CHECK(have >= need, LORA_EWORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", have, need);
-  CHECK(need == 0 || ws != nullptr, LORA_EWORKSPACE, "workspace is NULL");
-  CHECK(aligned(ws, 16), LORA_EALIGN, "workspace is not 16-byte aligned");
-  return LORA_OK;
-}
 
 // fp32 LoRA-gradient mode: each call first casts its fp32 adapters to bf16
 // (round to nearest even) into its workspace and then runs the bf16 path on

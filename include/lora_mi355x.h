@@ -386,6 +386,69 @@ lora_status lora_o_bwd(const lora_o_desc* desc, const void* dY, const void* X, c
                        size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Norms before and after a block, with its gate and the residual            */
+/* ------------------------------------------------------------------------ */
+
+/* Gate g of a block's output: none (1), one value per column [H] (a parameter,
+ * in the parameter dtype), per row [T], or per element [T, H] (both in the
+ * activation dtype). */
+typedef enum lora_gate {
+  LORA_GATE_NONE = 0,
+  LORA_GATE_COL = 1,
+  LORA_GATE_ROW = 2,
+  LORA_GATE_ELEM = 3
+} lora_gate;
+
+/* LORA_BF16: activations and parameters in bf16.  LORA_F32: all fp32.
+ * LORA_BF16_F32LORA: bf16 activations, fp32 parameters (w_post, w_pre, a
+ * column gate) and parameter gradients.  H is at most 16384, a positive
+ * multiple of 64 in the bf16 modes; T is any count, and [T, H] tensors may
+ * exceed 2 GiB.  All arithmetic is fp32; each output is rounded once. */
+typedef struct lora_norm_desc {
+  int64_t T;            /* rows */
+  int64_t H;            /* width of a row */
+  float eps;            /* added to the mean square, >= 0 */
+  float res_scale;      /* a */
+  float branch_scale;   /* b */
+  int32_t unit_offset;  /* o: 1 = the norms multiply by 1 + w, 0 = by w */
+  int32_t gate;         /* lora_gate */
+  int32_t dtype;
+  int32_t reserved;     /* must be 0 */
+} lora_norm_desc;
+
+typedef struct lora_norm_grads {
+  void* dgate;
+  void* dw_post;
+  void* dw_pre;
+} lora_norm_grads;
+
+lora_status lora_block_norm_workspace_size(const lora_norm_desc* desc, size_t* bwd_bytes);
+
+/* n(v) = v / sqrt(mean(v^2) + eps) over a row.
+ *   p = n(Y) (o + w_post), or Y where w_post is NULL;
+ *   R_out = a R + b g p;
+ *   X = n(R_out) (o + w_pre)   (from the unrounded R_out).
+ * Y NULL: no block output (the first norm of a model): X = n(R) (o + w_pre),
+ * R_out must be NULL, res_scale 1.  w_pre NULL: no X (which must be NULL).
+ * An output may be exactly one of the [T, H] inputs (R_out = R adds the block
+ * in place); any other overlap returns LORA_EUNSUPPORTED. */
+lora_status lora_block_norm_fwd(const lora_norm_desc* desc, const void* R, const void* Y, const void* gate,
+                                const void* w_post, const void* w_pre, void* R_out, void* X, void* stream);
+
+/* Gradients, given dR_out (NULL: zero) and dX of the forward's outputs, its
+ * R_out (read only with w_pre; without Y: the forward's R) and its Y (its
+ * values are read only with w_post or a gate; non-NULL exactly when the
+ * forward had one):
+ *   d = dR_out + gradient through X;  dR = a d;  dY = gradient through p of b g d;
+ *   dw_pre, dw_post, dgate as w_pre, w_post and the gate.
+ * Outputs are overwritten; T = 0 zero-fills the parameter gradients.  A
+ * [T, H] output may be exactly one of the [T, H] inputs; any other overlap
+ * returns LORA_EUNSUPPORTED. */
+lora_status lora_block_norm_bwd(const lora_norm_desc* desc, const void* dR_out, const void* dX, const void* R_out,
+                                const void* Y, const void* gate, const void* w_post, const void* w_pre, void* dR,
+                                void* dY, const lora_norm_grads* grads, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* NF4 format ([LL] "Use", QLoRA paragraphs)                                 */
 /* ------------------------------------------------------------------------ */
 
