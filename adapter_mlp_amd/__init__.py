@@ -23,6 +23,7 @@ __all__ = [
     "relu2_mlp_fwd", "relu2_mlp_bwd", "relu2_mlp_workspace_size",
     "qkv_fwd", "qkv_bwd", "o_fwd", "o_bwd", "o_fwd_noalloc",
     "block_norm_fwd", "block_norm_bwd", "block_norm_workspace_size",
+    "orthogonalize", "muon_step", "orth_workspace_size",
     "nf4_quantize", "nf4_dequant", "nf4_unpack_codes", "nf4_gemm", "nf4_codebook",
     "trace_begin", "trace_end",
 ]
@@ -707,6 +708,110 @@ def block_norm_bwd(dR_out, dX, R_out, Y=None, *, w_pre=None, w_post=None, gate=N
     _call_on(R_out, stream, "lora_block_norm_bwd", C.byref(d), _ptr(dR_out), _ptr(dX), _ptr(R_out), _ptr(Y), _ptr(gate),
              _ptr(w_post), _ptr(w_pre), _ptr(dR), _ptr(dY), C.byref(gr), _ptr(ws), _nbytes(ws, R_out.device))
     return dR, dY, grads
+
+
+# ---------------------------------------------------------------------------
+# Orthogonalised adapter updates
+# ---------------------------------------------------------------------------
+
+NS_COEFFS = (3.4445, -4.7750, 2.0315)
+
+
+def _stacks(name, ts, like=None, dtype=None):
+    """ts as a list of dense [rows, cols] or [count, rows, cols] tensors; with ``like``, of its shapes and device."""
+    torch = _torch()
+    ts = [ts] if torch.is_tensor(ts) else list(ts)
+    if like is not None and len(ts) != len(like):
+        raise ValueError(f"{name} holds {len(ts)} tensors, expected {len(like)}")
+    for i, t in enumerate(ts):
+        if t.dim() not in (2, 3):
+            raise ValueError(f"{name}[{i}] must be [rows, cols] or [count, rows, cols], got shape {tuple(t.shape)}")
+        _need(f"{name}[{i}]", t, (t if like is None else like[i]).shape, dtype or ts[0].dtype,
+              (ts if like is None else like)[0].device)
+    return ts
+
+
+def _orth_mats(P, G, M, scale):
+    mats = (L.lora_orth_mat * max(len(G), 1))()
+    for m, p, g, s, k in zip(mats, P, G, M or [None] * len(G), scale):
+        shape = g.shape
+        m.G, m.M, m.P = g.data_ptr(), None if s is None else s.data_ptr(), p.data_ptr()
+        m.count, m.rows, m.cols = (1, *shape) if len(shape) == 2 else shape
+        m.scale = k
+    return mats
+
+
+def _orth_desc(n, steps, coeffs, eps, dtype):
+    a, b, c = coeffs
+    return L.lora_orth_desc(n, steps, a, b, c, eps, dtype, 0)
+
+
+def _orth_ws(desc, mats):
+    n = C.c_size_t()
+    L.call("lora_orth_workspace_size", C.byref(desc), mats, C.byref(n))
+    return n.value
+
+
+def orth_workspace_size(mats):
+    """Bytes of workspace of orthogonalize or muon_step for these matrices."""
+    G = _stacks("mats", mats)
+    if not G:
+        return 0
+    return _orth_ws(_orth_desc(len(G), 1, NS_COEFFS, 0.0, _dtype_code(G[0])), _orth_mats(G, G, None, [1.0] * len(G)))
+
+
+def orthogonalize(mats, *, steps=5, coeffs=NS_COEFFS, eps=1e-7, out=None, ws=None, stream=None):
+    """Newton-Schulz steps X <- a X + (b S + c S S) X, S = X X^T, from X = G / (|G| + eps), for every matrix of
+    ``mats``: one tensor or a list of them, each [rows, cols] or a stack [count, rows, cols] with one side at
+    most 64 (adapters or their gradients), bf16 or fp32.  Returns the same structure; ``out`` (or mats itself)
+    receives the results."""
+    torch = _torch()
+    one = torch.is_tensor(mats)
+    G = _stacks("mats", mats)
+    if not G:
+        return []
+    desc = _orth_desc(len(G), steps, coeffs, eps, _dtype_code(G[0]))
+    P = _stacks("out", out, G, G[0].dtype) if out is not None else None
+    _on_gpu(G[0], ws)
+    with _on(stream):
+        if P is None:
+            P = [torch.empty_like(g) for g in G]
+        table = _orth_mats(P, G, None, [1.0] * len(G))
+        if ws is None:
+            ws = _ws(_orth_ws(desc, table), G[0].device)
+    _call_on(G[0], stream, "lora_orthogonalize", C.byref(desc), table, _ptr(ws), _nbytes(ws, G[0].device))
+    return P[0] if one else P
+
+
+def muon_step(params, grads, moms, *, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scale=None, steps=5,
+              coeffs=NS_COEFFS, eps=1e-7, ws=None, stream=None):
+    """One optimizer step with orthogonalised updates, in place on params and moms:
+
+        M <- momentum M + G;   U = G + momentum M (nesterov) or M
+        P <- (1 - lr weight_decay) P - lr scale orthogonalize(U)
+
+    params, grads (one dtype, bf16 or fp32) and moms (fp32) are tensors or lists as orthogonalize takes them.
+    scale: a factor per entry of the list, one for all, or None: sqrt(max(1, cols / rows)), which for W [n_in,
+    n_out] layouts gives updates of the same effect whatever the shape."""
+    P = _stacks("params", params)
+    if not P:
+        return
+    G = _stacks("grads", grads, P, P[0].dtype)
+    M = _stacks("moms", moms, P, _torch().float32)
+    if scale is None:
+        scale = [max(1.0, p.shape[-1] / p.shape[-2]) ** 0.5 for p in P]
+    elif isinstance(scale, (int, float)):
+        scale = [scale] * len(P)
+    elif len(scale) != len(P):
+        raise ValueError(f"scale holds {len(scale)} values, expected {len(P)}")
+    desc = L.lora_muon_desc(_orth_desc(len(P), steps, coeffs, eps, _dtype_code(P[0])), lr, momentum, weight_decay,
+                            int(nesterov), 0)
+    _on_gpu(P[0], ws)
+    table = _orth_mats(P, G, M, scale)
+    if ws is None:
+        with _on(stream):
+            ws = _ws(_orth_ws(desc.orth, table), P[0].device)
+    _call_on(P[0], stream, "lora_muon_step", C.byref(desc), table, _ptr(ws), _nbytes(ws, P[0].device))
 
 
 # ---------------------------------------------------------------------------

@@ -95,6 +95,21 @@ class lora_norm_grads(C.Structure):
     _fields_ = [("dgate", vp), ("dw_post", vp), ("dw_pre", vp)]
 
 
+class lora_orth_mat(C.Structure):
+    _fields_ = [("G", vp), ("M", vp), ("P", vp), ("count", i64), ("rows", i64), ("cols", i64), ("scale", C.c_float),
+                ("reserved", i32)]
+
+
+class lora_orth_desc(C.Structure):
+    _fields_ = [("n", i32), ("steps", i32), ("a", C.c_double), ("b", C.c_double), ("c", C.c_double), ("eps", C.c_double),
+                ("dtype", i32), ("reserved", i32)]
+
+
+class lora_muon_desc(C.Structure):
+    _fields_ = [("orth", lora_orth_desc), ("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double),
+                ("nesterov", i32), ("reserved", i32)]
+
+
 P = C.POINTER
 SIGNATURES = {
     "lora_version": (i32, []),
@@ -123,6 +138,9 @@ SIGNATURES = {
     "lora_block_norm_workspace_size": (i32, [P(lora_norm_desc), P(sz)]),
     "lora_block_norm_fwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp]),
     "lora_block_norm_bwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp, P(lora_norm_grads), vp, sz, vp]),
+    "lora_orth_workspace_size": (i32, [P(lora_orth_desc), P(lora_orth_mat), P(sz)]),
+    "lora_orthogonalize": (i32, [P(lora_orth_desc), P(lora_orth_mat), vp, sz, vp]),
+    "lora_muon_step": (i32, [P(lora_muon_desc), P(lora_orth_mat), vp, sz, vp]),
     "lora_nf4_quantize_workspace_size": (i32, [i64, i64, P(sz)]),
     "lora_nf4_quantize": (i32, [vp, i64, i64, i32, vp, vp, vp, vp, vp, sz, vp]),
     "lora_nf4_dequant": (i32, [P(lora_nf4), vp, i32, vp]),

@@ -449,6 +449,56 @@ lora_status lora_block_norm_bwd(const lora_norm_desc* desc, const void* dR_out, 
                                 void* dY, const lora_norm_grads* grads, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Orthogonalised adapter updates                                            */
+/* ------------------------------------------------------------------------ */
+
+/* A stack of `count` dense matrices [rows, cols], one side at most 64: the
+ * adapters A [n_in, r] or B [r, n_out] of several layers or users.  G and P
+ * have the descriptor's dtype (LORA_F32 or LORA_BF16), aligned to it. */
+typedef struct lora_orth_mat {
+  const void* G;   /* gradient (read) */
+  float* M;        /* lora_muon_step: momentum, fp32 (updated); else NULL */
+  void* P;         /* lora_orthogonalize: the result; lora_muon_step: the parameter (updated) */
+  int64_t count, rows, cols;
+  float scale;     /* lora_muon_step: factor of this stack's update */
+  int32_t reserved; /* must be 0 */
+} lora_orth_mat;
+
+typedef struct lora_orth_desc {
+  int32_t n;       /* entries of mats[] (host memory, read during the call) */
+  int32_t steps;   /* Newton-Schulz steps, 1 .. 32 */
+  double a, b, c;  /* coefficients of a step */
+  double eps;      /* added to the norm, >= 0 */
+  int32_t dtype;
+  int32_t reserved; /* must be 0 */
+} lora_orth_desc;
+
+typedef struct lora_muon_desc {
+  lora_orth_desc orth;
+  double lr, momentum, weight_decay;
+  int32_t nesterov; /* 1: U = G + momentum M, 0: U = M */
+  int32_t reserved; /* must be 0 */
+} lora_muon_desc;
+
+lora_status lora_orth_workspace_size(const lora_orth_desc* desc, const lora_orth_mat* mats, size_t* bytes);
+
+/* P = NS(G) for every matrix of every stack by itself:
+ *   X_0 = G / (|G| + eps)   (Frobenius norm)
+ *   X <- a X + (b S + c S S) X,  S = X X^T,   `steps` times
+ * (for a tall G with the products on its other side).  Formed in fp64, rounded
+ * once.  A matrix of zeros gives zeros.  P may be G itself; any other overlap
+ * returns LORA_EUNSUPPORTED. */
+lora_status lora_orthogonalize(const lora_orth_desc* desc, const lora_orth_mat* mats, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/* One optimizer step of every stack:
+ *   M <- momentum M + G;  U = G + momentum M (nesterov) or M   (fp32)
+ *   P <- (1 - lr weight_decay) P - lr scale NS(U)              (rounded once)
+ * No tensor may overlap another (LORA_EUNSUPPORTED). */
+lora_status lora_muon_step(const lora_muon_desc* desc, const lora_orth_mat* mats, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* NF4 format ([LL] "Use", QLoRA paragraphs)                                 */
 /* ------------------------------------------------------------------------ */
 
