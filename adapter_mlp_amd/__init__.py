@@ -22,6 +22,7 @@ __all__ = [
     "mlp_fwd", "mlp_bwd", "mlp_workspace_size",
     "relu2_mlp_fwd", "relu2_mlp_bwd", "relu2_mlp_workspace_size",
     "qkv_fwd", "qkv_bwd", "o_fwd", "o_bwd", "o_fwd_noalloc",
+    "AdapterPool", "multi_fwd", "multi_workspace_size",
     "block_norm_fwd", "block_norm_bwd", "block_norm_workspace_size",
     "orthogonalize", "muon_step", "orth_workspace_size",
     "nf4_quantize", "nf4_dequant", "nf4_unpack_codes", "nf4_gemm", "nf4_codebook",
@@ -587,7 +588,7 @@ def o_bwd(dY, X, U, o: Proj, *, dX=None, dA=None, dB=None, ws=None, stream=None,
 
 
 # ---------------------------------------------------------------------------
-# Norms before and after a block
+# Adapters of many requests beside one shared projection
 # ---------------------------------------------------------------------------
 
 def _call_on(t, stream, name, *args):
@@ -605,6 +606,62 @@ def _call_on(t, stream, name, *args):
         with torch.cuda.device(dev):
             L.call(name, *args, stream.cuda_stream)
 
+
+@dataclass
+class AdapterPool:
+    """Adapters of one projection, stacked: A [n, n_in, r], B [n, r, n_out] and their scales [n] (fp32)."""
+
+    A: object
+    B: object
+    scale: object
+
+
+def multi_workspace_size(T, K, N, r, n, dtype=L.LORA_BF16):
+    d = L.lora_multi_desc(T, K, N, r, n, dtype, 0)
+    b = C.c_size_t()
+    L.call("lora_multi_workspace_size", C.byref(d), C.byref(b))
+    return b.value
+
+
+def multi_fwd(X, W, pool: AdapterPool, ids, *, Y=None, ws=None, stream=None):
+    """Y[t] = X[t] W + scale[i] (X[t] A[i]) B[i] with i = ids[t], for X [T, n_in], W [n_in, n_out] and ids [T]
+    (int32, on the GPU, rows in any order); a row whose id is outside [0, n) takes the base alone.
+
+    With W None the adapter terms are added to Y in place: Y then holds the product with a base kept in another
+    form (``nf4_gemm``).  Returns Y."""
+    torch = _torch()
+    T, K = _x2d("X", X)
+    if pool.A.dim() != 3 or pool.B.dim() != 3:
+        raise ValueError("pool.A must be [n, n_in, r] and pool.B [n, r, n_out]")
+    n, _, r = pool.A.shape
+    N = pool.B.shape[2]
+    dt = _dtype_code(X)
+    _need("X", X, (T, K), X.dtype, X.device)
+    if W is not None:
+        _need("W", W, (K, N), X.dtype, X.device)
+    _need("pool.A", pool.A, (n, K, r), X.dtype, X.device)
+    _need("pool.B", pool.B, (n, r, N), X.dtype, X.device)
+    _need("pool.scale", pool.scale, (n,), torch.float32, X.device)
+    _need("ids", ids, (T,), torch.int32, X.device)
+    if Y is not None:
+        _need("Y", Y, (T, N), X.dtype, X.device)
+    elif W is None:
+        raise ValueError("without W the adapter terms are added to Y, which is missing")
+    _on_gpu(X, ws)
+    d = L.lora_multi_desc(T, K, N, r, n, dt, 0)
+    with _on(stream):
+        if Y is None:
+            Y = torch.empty((T, N), dtype=X.dtype, device=X.device)
+        if ws is None:
+            ws = _ws(multi_workspace_size(T, K, N, r, n, dt), X.device)
+    _call_on(X, stream, "lora_multi_fwd", C.byref(d), _ptr(X), _ptr(W), _ptr(pool.A), _ptr(pool.B), _ptr(pool.scale),
+             _ptr(ids), _ptr(Y), _ptr(ws), _nbytes(ws, X.device))
+    return Y
+
+
+# ---------------------------------------------------------------------------
+# Norms before and after a block
+# ---------------------------------------------------------------------------
 
 def _norm_call(R, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset):
     """The checked descriptor of a block norm over rows like R's."""

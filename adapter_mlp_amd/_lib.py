@@ -86,6 +86,10 @@ class lora_o_desc(C.Structure):
                 ("plan", C.POINTER(lora_plan))]
 
 
+class lora_multi_desc(C.Structure):
+    _fields_ = [("T", i64), ("K", i64), ("N", i64), ("r", i64), ("n", i64), ("dtype", i32), ("reserved", i32)]
+
+
 class lora_norm_desc(C.Structure):
     _fields_ = [("T", i64), ("H", i64), ("eps", C.c_float), ("res_scale", C.c_float), ("branch_scale", C.c_float),
                 ("unit_offset", i32), ("gate", i32), ("dtype", i32), ("reserved", i32)]
@@ -135,6 +139,8 @@ SIGNATURES = {
     "lora_o_fwd": (i32, [P(lora_o_desc), vp, P(lora_proj), vp, vp, vp, sz, vp]),
     "lora_o_bwd": (i32, [P(lora_o_desc), vp, vp, vp, P(lora_proj), vp, vp, vp, vp, sz, vp]),
     "lora_o_fwd_noalloc": (i32, [P(lora_o_desc), vp, P(lora_proj), vp, vp, vp]),
+    "lora_multi_workspace_size": (i32, [P(lora_multi_desc), P(sz)]),
+    "lora_multi_fwd": (i32, [P(lora_multi_desc), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
     "lora_block_norm_workspace_size": (i32, [P(lora_norm_desc), P(sz)]),
     "lora_block_norm_fwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp]),
     "lora_block_norm_bwd": (i32, [P(lora_norm_desc), vp, vp, vp, vp, vp, vp, vp, vp, vp, P(lora_norm_grads), vp, sz, vp]),

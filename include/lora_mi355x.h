@@ -386,6 +386,35 @@ lora_status lora_o_bwd(const lora_o_desc* desc, const void* dY, const void* X, c
                        size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Adapters of many requests beside one shared projection                    */
+/* ------------------------------------------------------------------------ */
+
+/* A batch whose rows belong to different adapters of the same projection:
+ * n adapters of one rank are stacked as A [n, K, r] and B [n, r, N], and ids
+ * [T] names each row's.  LORA_BF16 or LORA_F32. */
+typedef struct lora_multi_desc {
+  int64_t T;   /* rows of X: tokens of all requests */
+  int64_t K;   /* input width n_in */
+  int64_t N;   /* output width n_out */
+  int64_t r;   /* rank of the adapters */
+  int64_t n;   /* adapters in the stacks (0: none, A, B and scales may be NULL) */
+  int32_t dtype;
+  int32_t reserved; /* must be 0 */
+} lora_multi_desc;
+
+lora_status lora_multi_workspace_size(const lora_multi_desc* desc, size_t* bytes);
+
+/* Y[t] = X[t] W + scales[i] (X[t] A[i]) B[i], i = ids[t]; a row whose id lies
+ * outside [0, n) takes X[t] W alone.  W [K, N] dense, scales [n] fp32 and ids
+ * [T] int32 in device memory; rows may come in any order and number per
+ * adapter.  W NULL: the adapter terms are added to what Y holds (the product
+ * with a base kept in another form, e.g. lora_nf4_gemm's).  Each adapter, W,
+ * X and Y must be smaller than 2 GiB - 4 KiB; the stacks may be larger.  No
+ * output may overlap an input (LORA_EUNSUPPORTED). */
+lora_status lora_multi_fwd(const lora_multi_desc* desc, const void* X, const void* W, const void* A, const void* B,
+                           const float* scales, const int32_t* ids, void* Y, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Norms before and after a block, with its gate and the residual            */
 /* ------------------------------------------------------------------------ */
 
