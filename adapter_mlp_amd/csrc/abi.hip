@@ -202,6 +202,13 @@ int64_t ksplit_t0(int64_t tiles, int s) {
   return (s > 1 && R > 0 && rem > 0) ? R * 256 : 0;
 }
 
+}  // namespace
+
+int lora::store_gemm_ksplit(int64_t M, int64_t N, int64_t K) { return gemm_ksplit(Ctx{true, false, 2}, M, N, K); }
+int64_t lora::store_gemm_split_from(int64_t tiles, int ksplit) { return ksplit_t0(tiles, ksplit); }
+
+namespace {
+
 // fp32 partial floats a split store GEMM needs (0 without a split); `forced`
 // is the plan's ksplit (0: the model above).
 int64_t kpart_floats(const Ctx& c, int64_t M, int64_t N, int64_t K, int forced = 0) {

@@ -846,8 +846,11 @@ constexpr int SPARE = CODE_RING + 3 * CODE_SLOT;  // target of the stores of an 
 constexpr int SPARE_BYTES = 2048;
 static_assert(SPARE + SPARE_BYTES <= LDS_BYTES, "NF4 code ring exceeds LDS");
 
-template <int BKIND, bool DUAL, int EPI, bool NF4, int ACT>
+// MULTI (plain store of dense NN weights): rows belong to different adapters,
+// which join after the K loop (see the adapter phase below).
+template <int BKIND, bool DUAL, int EPI, bool NF4, int ACT, bool MULTI>
 __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
+  static_assert(!MULTI || (BKIND == B_NN && !DUAL && EPI == EPI_STORE && !NF4), "adapters per row: dense NN store");
   static_assert(!(DUAL && BKIND == B_NT && NF4), "NF4 gate/up tiles read forward (NN) weights");
   __shared__ __attribute__((aligned(1024))) char smem_raw[LDS_BYTES];
   lds_char* const lds = (lds_char*)smem_raw;
@@ -1609,6 +1612,101 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
     }
   }
 
+  // ---- adapters per row (MULTI) ----
+  // Once the operand slots are free: the tile's rows of U [M, 64] go to an
+  // activation slot, once; then for each adapter of the tile, B_i (its r rows, zeros up to a multiple of 32) goes through the
+  // weight ring, is multiplied with the 16-row blocks that hold rows of it, and
+  // the products are added where the row (one per lane) is its own.  Selecting
+  // instead of multiplying by zeros keeps an adapter that holds infinities to
+  // its own rows, and costs eight vector instructions per two MFMAs in the
+  // blocks concerned.  The sums reach the epilogue unrounded.
+  if constexpr (MULTI) {
+    if (args.mt_plan != nullptr && kp <= 0) {
+      const MultiTile& T = args.mt_plan[tm];
+      const int count = __builtin_amdgcn_readfirstlane(T.count);
+      const int ksteps = args.mt_r > 32 ? 2 : 1;
+      const int r = args.mt_r;
+      // loads of B_i: block b of 1 KB holds K rows 4 (b % 16) .. + 3 of column half b / 16;
+      // wavefront w takes blocks with b % 16 = w, w + 8 (of those below 8 ksteps) of both halves
+      const int64_t col0 = tnl * 256;
+      const uint32_t ldb2 = (uint32_t)(NR * 2);
+      const uint32_t boff = (uint32_t)(lane >> 4) * ldb2 + (uint32_t)(((lane & 15) ^ (4 * ((lane >> 4) & 3))) << 4);
+      // lane l holds the table entries of slots s0 + l (s0 the current multiple of 64), so that
+      // no table load waits for the operand loads in flight
+      int ids = 0, blk = 0, sl[8];
+      auto table = [&](int s0) {
+        ids = T.id[s0 + lane];
+        blk = (int)T.blocks[s0 + lane];
+        asm volatile("" : "+v"(ids), "+v"(blk));
+      };
+      auto issue_b = [&](int s, int idv) {
+        const int64_t id = idv;
+        const char* B = static_cast<const char*>(args.mt_b) + id * r * NR * 2;
+        const uint32_t slot = lds_addr(lds) + W_RING + (uint32_t)(s % 3) * SLOT_BYTES;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            if (b < ksteps) {
+              const int row = 4 * (wave + 8 * b);  // rows past r read zero
+              const int64_t first = ((int64_t)row * NR + col0 + 128 * h) * 2;
+              dma16(rsrc_words(B + first, (int64_t)r * NR * 2 - first), boff, slot + h * HALF_BYTES + (wave + 8 * b) * 1024);
+            }
+      };
+      if (count > 0) {
+        table(0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          sl[j] = T.slot[wm * 128 + 16 * j + (lane & 15)];
+          asm volatile("" : "+v"(sl[j]));
+        }
+      }
+      if (count > 0) {
+        const i32x4 ru = rsrc_words(static_cast<const char*>(args.mt_u) + m0 * 128, (M - m0) * 128);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          dma16(ru, (uint32_t)((8 * (4 * wave + i) + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)),
+                lds_addr(lds) + (4 * wave + i) * 1024);
+        issue_b(0, __builtin_amdgcn_readlane(ids, 0));
+        for (int s = 0; s < count; ++s) {
+          const uint32_t rows = (uint32_t)__builtin_amdgcn_readlane(blk, s & 63) >> (8 * wm);
+          if (s + 1 < count) {
+            if (((s + 1) & 63) == 0) table(s + 1);
+            issue_b(s + 1, __builtin_amdgcn_readlane(ids, (s + 1) & 63));
+            if (ksteps == 2) wait_vmcnt<4>();
+            else wait_vmcnt<2>();
+          } else {
+            wait_vmcnt<0>();
+          }
+          // B_s (and U) is in for every wavefront, and B_{s-2}'s slot is no longer read
+          __syncthreads();
+          const lds_char* const wt = lds + W_RING + (s % 3) * SLOT_BYTES;
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            if (ks < ksteps)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                fa[4 * ks + i] = lds_read_tr8(wt + fa_nn[i >> 1] + 32 * (i & 1) + (32 * ks) * 256, 4 * 256);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (((rows >> j) & 1) == 0) continue;  // uniform
+            const bool own = sl[j] == s;
+            const bf16x8 u0 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(0, j)] + 2048 * j));
+            const bf16x8 u1 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(1, j)] + 2048 * j));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, f32x4{0, 0, 0, 0}, 0, 0, 0);
+              if (ksteps == 2) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], u1, d, 0, 0, 0);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[i][j][v] = own ? acc[i][j][v] + d[v] : acc[i][j][v];
+            }
+          }
+        }
+        __syncthreads();  // the slots become epilogue staging
+      }
+    }
+  }
+
 #ifdef LORA_PHASE_TIMING
   if ((wave == 0 || wave == 4) && lane == 0 && blockIdx.x < 64u) {
     constexpr int fam = (NF4 ? 4 : 0) + ((EPI == EPI_ACT_FWD || EPI == EPI_ACT1_FWD) ? 0
@@ -1676,12 +1774,12 @@ __global__ void ksplit_reduce_kernel(const float* part, int ks, int64_t M, int64
   *reinterpret_cast<u32x4*>(out + m * ldo + n) = v;
 }
 
-template <int BKIND, bool DUAL, int EPI, bool NF4, int ACT = 0>
+template <int BKIND, bool DUAL, int EPI, bool NF4, int ACT = 0, bool MULTI = false>
 hipError_t launch(const GemmArgs& a, hipStream_t st) {
   const int64_t nt = a.ntile_m * a.ntile_n;
   const int64_t nb = a.ksplit > 1 && !NF4 ? a.ksplit_t0 + (nt - a.ksplit_t0) * a.ksplit : nt;
   if (nb == 0) return hipSuccess;
-  hipLaunchKernelGGL((gemm_kernel<BKIND, DUAL, EPI, NF4, ACT>), dim3((unsigned)nb), dim3(NTH8), 0, st, a);
+  hipLaunchKernelGGL((gemm_kernel<BKIND, DUAL, EPI, NF4, ACT, MULTI>), dim3((unsigned)nb), dim3(NTH8), 0, st, a);
   return hipGetLastError();
 }
 
@@ -1692,6 +1790,9 @@ hipError_t launch_family(const GemmArgs& a, hipStream_t st) {
       return a.act == LORA_ACT_SWIGLU ? launch<B_NN, true, EPI_ACT_FWD, NF4, LORA_ACT_SWIGLU>(a, st)
                                       : launch<B_NN, true, EPI_ACT_FWD, NF4, LORA_ACT_GEGLU_TANH>(a, st);
     if (a.epi == EPI_ACT1_FWD) return launch<B_NN, false, EPI_ACT1_FWD, NF4>(a, st);
+    if constexpr (!NF4) {
+      if (a.mt_plan != nullptr) return launch<B_NN, false, EPI_STORE, false, 0, true>(a, st);
+    }
     return launch<B_NN, false, EPI_STORE, NF4>(a, st);
   }
   if constexpr (!NF4) {  // forward GEMMs over K-contiguous weights (dense only)

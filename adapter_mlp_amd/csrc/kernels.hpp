@@ -119,12 +119,33 @@ struct GemmArgs {
   int64_t rc_ldu;
   int32_t rc_uoff[2];
   int32_t rc_R, pad5_;
+  // EPI_STORE, bf16, dense NN, one region, with mt_plan set: each row's own
+  // adapter is added to the sums before they are rounded: row m takes
+  // U[m] B_i, U = mt_u [M, 64] (scaled, zero past the rank), B_i = mt_b [n, mt_r, N],
+  // i by the plan of the row's 256-row tile (MultiTile).
+  const void* mt_u;
+  const void* mt_b;
+  const struct MultiTile* mt_plan;
+  int32_t mt_r, pad6_;
+};
+
+// The adapters of one 256-row tile, in ascending order.
+struct MultiTile {
+  int32_t count;
+  int32_t pad_[3];
+  int32_t id[256];       // adapter of slot s < count
+  uint32_t blocks[256];  // its 16-row blocks, one bit each
+  int32_t slot[256];     // slot of each row (-1: none, also past the last row)
 };
 
 // Columns of output covered by one n-tile.
 int64_t gemm_tile_cols(bool bf16, bool dual);
 int64_t gemm_tile_rows(bool bf16);
 hipError_t launch_gemm_bf16(const GemmArgs& a, hipStream_t st);
+// The split-K factor that the calls take by default for a bf16 store GEMM
+// [M, N] over K with one region, and the first tile to split (abi.hip).
+int store_gemm_ksplit(int64_t M, int64_t N, int64_t K);
+int64_t store_gemm_split_from(int64_t tiles, int ksplit);
 // For the split tiles of a (tiles ksplit_t0 ..): out[m, n] (bf16) = sum over
 // k < ksplit, ascending, of kpart[k][m][n]
 hipError_t launch_ksplit_reduce(const GemmArgs& a, hipStream_t st);

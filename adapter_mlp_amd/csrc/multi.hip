@@ -19,7 +19,9 @@ struct MultiArgs {
   float* part;   // [ks, T, N] fp32 sums of X W over K ranges (nullptr: add to Y)
   float* upart;  // [kc, T, r] fp32 sums of X A_i over K ranges
   int64_t T, K, N, n;
-  int32_t r, ks, kc, ntn, ntm;
+  int32_t r, ks, kc, ntn;
+  uint16_t* u;       // [T, 64] bf16: scaled U, zero past the rank (many rows)
+  MultiTile* plan;   // adapters of every 256-row tile (many rows)
 };
 
 // The adapter of a row, -1 for none.
@@ -48,8 +50,11 @@ __device__ __forceinline__ void wait_stages(int after) {
 // streaming W once, so the work is split over K until the grid fills the
 // chip, and every block keeps several 64-deep K stages in flight: W
 // [64][128 columns] and X [16 MT rows][64] go from global memory straight into
-// a ring of LDS slots.  Four wavefronts of 32 columns each; the weight is the
-// MFMA's row operand, so a lane ends with four consecutive columns of a row.
+// a ring of LDS slots.  Wavefront (h, k) of four takes column half h and
+// K half k of every stage (no operand is read from LDS more often than it
+// must for 64 x 16 MT sums a wavefront), and the two K halves meet at the
+// end.  The weight is the MFMA's row operand, so a lane ends with four
+// consecutive columns of a row.
 // LDS layouts: W rows of 256 bytes, 16-byte chunk c of row k at c ^ 4 (k & 3),
 // read with the transposing LDS read; X rows of 128 bytes, chunk c of row m at
 // c ^ (m & 7).
@@ -57,9 +62,11 @@ __device__ __forceinline__ void wait_stages(int after) {
 template <int MT>
 struct BaseCfg {
   static constexpr int WB = 64 * 256, XB = MT * 16 * 128, SB = WB + XB;
-  static constexpr int NST = MT <= 4 ? 4 : 3;
-  static constexpr int XPW = MT / 2;  // 1 KB loads of X per wavefront and stage
-  static constexpr int D = 4 + XPW;
+  // two blocks a CU while three stages fit half of its LDS, else one with five
+  static constexpr int PER_CU = 3 * SB <= 81920 ? 2 : 1;
+  static constexpr int NST = PER_CU == 2 ? (4 * SB <= 81920 ? 4 : 3) : 5;
+  static constexpr int SMEM = NST * SB > 2 * MT * 4096 ? NST * SB : 2 * MT * 4096;
+  static_assert(SMEM * PER_CU <= 163840, "LDS of a CU");
 };
 
 template <int MT>
@@ -68,26 +75,24 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
   lds_char* const lds = (lds_char*)ring;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // blocks b, b + 8, ... run on one XCD: the row tiles of one weight tile follow each other there
-  const int units = a.ntn * a.ks;
-  const int j = bid >> 3;
-  const int u = (j / a.ntm) * 8 + (bid & 7), tm = j % a.ntm;
-  if (u >= units) return;
-  const int tn = u % a.ntn, part = u / a.ntn;
+  const int h = w & 1, kh = w >> 1;
+  const int tn = bid % a.ntn, part = bid / a.ntn;
   const int steps = (int)(a.K / 64);
   const int s0 = (int)((int64_t)part * steps / a.ks), s1 = (int)((int64_t)(part + 1) * steps / a.ks);
-  const int64_t m0 = (int64_t)tm * (16 * MT), n0 = (int64_t)tn * 128;
+  const int64_t n0 = (int64_t)tn * 128;
   const uint32_t ldw2 = (uint32_t)(a.N * 2), ldx2 = (uint32_t)(a.K * 2);
   const char* wp = static_cast<const char*>(a.W) + ((int64_t)s0 * 64 * a.N + n0) * 2;
   int64_t wn = ((a.K - (int64_t)s0 * 64) * a.N - n0) * 2;
-  const char* xp = static_cast<const char*>(a.X) + (m0 * a.K + (int64_t)s0 * 64) * 2;
-  int64_t xn = ((a.T - m0) * a.K - (int64_t)s0 * 64) * 2;
+  const char* xp = static_cast<const char*>(a.X) + (int64_t)s0 * 128;
+  int64_t xn = (a.T * a.K - (int64_t)s0 * 64) * 2;
   const uint32_t woff = (uint32_t)(lane >> 4) * ldw2 + (uint32_t)(((lane & 15) ^ (4 * ((lane >> 4) & 3))) * 16);
-  uint32_t xoff[C::XPW];  // rows past T read zero
+  // X block b of 1 KB holds rows 8 b .. 8 b + 7; wavefront w loads blocks w, w + 4, ... of 2 MT
+  constexpr int XP = (2 * MT + 3) / 4;
+  uint32_t xoff[XP];  // rows past T read zero
 #pragma unroll
-  for (int i = 0; i < C::XPW; ++i) {
-    const int row = 8 * (C::XPW * w + i) + (lane >> 3);
-    xoff[i] = m0 + row < a.T ? (uint32_t)row * ldx2 + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16) : 0x80000000u;
+  for (int i = 0; i < XP; ++i) {
+    const int row = 8 * (w + 4 * i) + (lane >> 3);
+    xoff[i] = row < a.T ? (uint32_t)row * ldx2 + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16) : 0x80000000u;
   }
   auto issue = [&](int slot) {
     const uint32_t base = lds_addr(lds) + slot * C::SB;
@@ -95,65 +100,78 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
 #pragma unroll
     for (int i = 0; i < 4; ++i) dma16(rw, woff, base + (4 * w + i) * 1024, (uint32_t)(4 * (4 * w + i)) * ldw2);
 #pragma unroll
-    for (int i = 0; i < C::XPW; ++i)
-      dma16(rx, xoff[i], base + C::WB + (C::XPW * w + i) * 1024);
+    for (int i = 0; i < XP; ++i)
+      if (w + 4 * i < 2 * MT) dma16(rx, xoff[i], base + C::WB + (w + 4 * i) * 1024);
     wp += (int64_t)64 * a.N * 2;
     wn -= (int64_t)64 * a.N * 2;
     xp += 128;
     xn -= 128;
   };
+  // an odd MT leaves the last X load to wavefronts 0 and 1
+  const bool fewer = (2 * MT) % 4 != 0 && w >= 2;
   const int g = lane >> 4, c = lane & 15, jj = c >> 2;
-  f32x4 acc[2][MT];
+  f32x4 acc[4][MT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[i][m] = f32x4{0, 0, 0, 0};
-  int wo[2];  // fragment offsets of the wavefront's two 16-column blocks
+  // fragment offsets of 16-column blocks 2 i and 2 i + 1 (bit 1 of the chunk index is clear in the
+  // first and in the swizzle, so the second is 32 bytes on)
+  int wo[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const int col = 32 * w + 16 * i + 4 * (lane & 3);
-    wo[i] = (8 * g + jj) * 256 + (((col >> 3) ^ (4 * jj)) * 16) + (lane & 1) * 8;
+    const int col = 64 * h + 32 * i + 4 * (lane & 3);
+    wo[i] = (32 * kh + 8 * g + jj) * 256 + (((col >> 3) ^ (4 * jj)) * 16) + (lane & 1) * 8;
   }
+  const int xo = c * 128 + (((4 * kh + g) ^ (c & 7)) * 16);
   const int n = s1 - s0;
   for (int s = 0; s < C::NST - 1 && s < n; ++s) issue(s);
   int slot = 0;
   for (int s = 0; s < n; ++s) {
     const int after = n - 1 - s < C::NST - 2 ? n - 1 - s : C::NST - 2;
-    wait_stages<C::D, C::NST - 2>(after);
+    if (fewer) wait_stages<4 + XP - 1, C::NST - 2>(after);
+    else wait_stages<4 + XP, C::NST - 2>(after);
     __syncthreads();  // stage s is in for every wavefront, and stage s - 1 is no longer read
     if (s + C::NST - 1 < n) issue(slot == 0 ? C::NST - 1 : slot - 1);
     const lds_char* ws = lds + slot * C::SB;
     const lds_char* xs = ws + C::WB;
+    bf16x8 fw[4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      bf16x8 fw[2], fx[MT];
+    for (int i = 0; i < 4; ++i) fw[i] = lds_read_tr8(ws + wo[i >> 1] + 32 * (i & 1), 4 * 256);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) fw[i] = lds_read_tr8(ws + wo[i] + 32 * k * 256, 4 * 256);
+    for (int m = 0; m < MT; ++m) {
+      const bf16x8 fx = __builtin_bit_cast(bf16x8, lds_read16(xs + xo + m * 2048));
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        fx[m] = __builtin_bit_cast(bf16x8, lds_read16(xs + (16 * m + c) * 128 + (((4 * k + g) ^ (c & 7)) * 16)));
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fx[m], acc[i][m], 0, 0, 0);
+      for (int i = 0; i < 4; ++i) acc[i][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw[i], fx, acc[i][m], 0, 0, 0);
     }
     slot = slot + 1 == C::NST ? 0 : slot + 1;
   }
-  float* out = a.part + (int64_t)part * a.T * a.N;
+  __syncthreads();  // the ring becomes the exchange of the K halves
+  f32x4* ex = reinterpret_cast<f32x4*>(ring) + h * (4 * MT * 64);
+  if (kh == 1)
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int64_t t = m0 + 16 * m + c;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t col = n0 + 32 * w + 16 * i + 4 * g;
-      if (t < a.T && col < a.N) *reinterpret_cast<f32x4*>(out + t * a.N + col) = acc[i][m];
+      for (int i = 0; i < 4; ++i) ex[(m * 4 + i) * 64 + lane] = acc[i][m];
+  __syncthreads();
+  if (kh == 0) {
+    float* out = a.part + (int64_t)part * a.T * a.N;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int64_t t = 16 * m + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t col = n0 + 64 * h + 16 * i + 4 * g;
+        const f32x4 v = acc[i][m] + ex[(m * 4 + i) * 64 + lane];
+        if (t < a.T && col < a.N) *reinterpret_cast<f32x4*>(out + t * a.N + col) = v;
+      }
     }
   }
 }
 
 template <int MT>
 __global__ __launch_bounds__(256) void multi_base_kernel(const MultiArgs a) {
-  __shared__ __attribute__((aligned(1024))) char ring[BaseCfg<MT>::NST * BaseCfg<MT>::SB];
+  __shared__ __attribute__((aligned(1024))) char ring[BaseCfg<MT>::SMEM];
   base_block<MT>(a, ring, blockIdx.x);
 }
 
@@ -162,47 +180,49 @@ __global__ __launch_bounds__(256) void multi_base_kernel(const MultiArgs a) {
 // block.  Every wavefront takes a quarter of the range for all of the rows
 // and walks the distinct adapters of the rows, each multiplied against all
 // of them (the MFMA computes 16 rows at a time anyway) and kept where it is
-// the row's own; rows of one request sit together, so that is one or two
-// passes over rows that stay in cache.  A_i [K, r] is read as it lies: lane
-// 16 q + c takes columns NJ c .. NJ c + NJ - 1 of 8 consecutive K rows, which
-// after a transpose in registers are the operands of NJ tiles (tile t: rank
-// index NJ c + t).
+// the row's own.  gridDim.z blocks share the walk.  With many rows (RG = 4)
+// the rows of a 256-row tile are first put in the order of their adapters, so
+// that 64 of them meet few.  A_i [K, r] is read as it lies: lane 16 q + c
+// takes columns NJ c .. NJ c + NJ - 1 of 8 consecutive K rows, which after a
+// transpose in registers are the operands of NJ tiles (tile t: rank index
+// NJ c + t).
 // ---------------------------------------------------------------------------
 constexpr int kShrinkK = 1024;
 
 template <int NJ>
-__device__ __forceinline__ void load_a_frags(brsrc ra, uint32_t row0, int r, int c, bf16x8 (&f)[NJ]) {
-  // row0: first of the lane's 8 K rows; rows past the end read zero
-  const uint32_t ld = (uint32_t)r * 2;
-  uint32_t off = row0 * ld + (uint32_t)(NJ * c) * 2;
-  if (NJ * c >= r) off = 0x80000000u;  // columns past the rank read zero
-  uint16_t x[8][NJ];
+struct AFrags {
+  uint32_t x[8][NJ];
+  // rows row0 .. row0 + 7 of A_i; rows past the end and columns past the rank read zero
+  __device__ __forceinline__ void load(brsrc ra, uint32_t row0, int r, int c) {
+    const uint32_t ld = (uint32_t)r * 2;
+    const bool in = NJ * c < r;
+    const uint32_t off = row0 * ld + (uint32_t)(NJ * c) * 2;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t o = off + (off < 0x80000000u ? (uint32_t)e * ld : 0u);
-    if constexpr (NJ == 4) {
-      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(ra, o, 0, 0);
-      x[e][0] = (uint16_t)v[0];
-      x[e][1] = (uint16_t)(v[0] >> 16);
-      x[e][2] = (uint16_t)v[1];
-      x[e][3] = (uint16_t)(v[1] >> 16);
-    } else if constexpr (NJ == 2) {
-      const uint32_t v = __builtin_amdgcn_raw_buffer_load_b32(ra, o, 0, 0);
-      x[e][0] = (uint16_t)v;
-      x[e][1] = (uint16_t)(v >> 16);
-    } else {
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t o = in ? off + (uint32_t)e * ld : 0x80000000u;
+      if constexpr (NJ == 4) {
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(ra, o, 0, 0);
+        x[e][0] = v[0];
+        x[e][1] = v[1];
+      } else if constexpr (NJ == 2) {
+        x[e][0] = __builtin_amdgcn_raw_buffer_load_b32(ra, o, 0, 0);
+      } else {
 #pragma unroll
-      for (int t = 0; t < NJ; ++t) x[e][t] = __builtin_amdgcn_raw_buffer_load_b16(ra, o + 2 * t, 0, 0);
+        for (int t = 0; t < NJ; ++t) x[e][t] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ra, o + 2 * t, 0, 0);
+      }
     }
   }
-#pragma unroll
-  for (int t = 0; t < NJ; ++t) {
+  // operand of tile t: element e of the lane is row row0 + e
+  __device__ __forceinline__ bf16x8 frag(int t) const {
     u32x4 v;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = (uint32_t)x[2 * e][t] | ((uint32_t)x[2 * e + 1][t] << 16);
-    f[t] = __builtin_bit_cast(bf16x8, v);
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (NJ == 1 || NJ == 3) v[e] = x[2 * e][t] | (x[2 * e + 1][t] << 16);
+      else v[e] = __builtin_amdgcn_perm(x[2 * e + 1][t >> 1], x[2 * e][t >> 1], (t & 1) ? 0x07060302u : 0x05040100u);
+    }
+    return __builtin_bit_cast(bf16x8, v);
   }
-}
+};
 
 template <int RG, int NJ>
 __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
@@ -210,23 +230,47 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * RG);
   const int kc = blockIdx.y;
   const int64_t k0 = (int64_t)kc * kShrinkK + w * (kShrinkK / 4);
   const int64_t klen = a.K - k0 < kShrinkK / 4 ? a.K - k0 : kShrinkK / 4;  // multiple of 64, may be <= 0
-  const int my = lane < 16 * RG ? row_id(a, t0 + lane) : -1;               // id of row t0 + lane
-  int rid[RG];                                                             // ids of this lane's MFMA rows
+  // row (relative to t0) and adapter of MFMA row `lane` (lane < 16 RG)
+  int64_t t0;
+  int my, myrow;
+  if constexpr (RG == 4) {
+    __shared__ int ids[256], row_of[256], id_of[256];
+    const int i = threadIdx.x;
+    t0 = (int64_t)(blockIdx.x >> 2) * 256;
+    const int id = row_id(a, t0 + i);
+    const int key = id < 0 ? 0x7fffffff : id;
+    ids[i] = key;
+    __syncthreads();
+    int rank = 0;
+#pragma unroll 8
+    for (int j = 0; j < 256; ++j) rank += ids[j] < key || (ids[j] == key && j < i);
+    row_of[rank] = i;
+    id_of[rank] = id;
+    __syncthreads();
+    myrow = row_of[64 * (blockIdx.x & 3) + lane];
+    my = id_of[64 * (blockIdx.x & 3) + lane];
+  } else {
+    t0 = (int64_t)blockIdx.x * (16 * RG);
+    myrow = lane & (16 * RG - 1);
+    my = lane < 16 * RG ? row_id(a, t0 + lane) : -1;
+  }
+  int rid[RG], row[RG];  // of this lane's MFMA rows
+  uint32_t xrow[RG];     // rows past T read zero
 #pragma unroll
-  for (int m = 0; m < RG; ++m) rid[m] = __shfl(my, 16 * m + c);
-  uint32_t xrow[RG];  // rows past T read zero
-#pragma unroll
-  for (int m = 0; m < RG; ++m)
-    xrow[m] = t0 + 16 * m + c < a.T ? (uint32_t)((16 * m + c) * a.K * 2) : 0x80000000u;
+  for (int m = 0; m < RG; ++m) {
+    rid[m] = __shfl(my, 16 * m + c);
+    row[m] = __shfl(myrow, 16 * m + c);
+    xrow[m] = t0 + row[m] < a.T ? (uint32_t)(row[m] * a.K * 2) : 0x80000000u;
+  }
   const brsrc rx = make_rsrc(static_cast<const char*>(a.X) + (t0 * a.K + k0) * 2, ((a.T - t0) * a.K - k0) * 2);
   uint64_t todo = __ballot(my >= 0);
-  while (todo != 0) {
+  for (int turn = 0; todo != 0; turn = turn + 1 == (int)gridDim.z ? 0 : turn + 1) {
     const int id = __builtin_amdgcn_readlane(my, __builtin_ctzll(todo));
     todo &= ~__ballot(my == id);
+    if (turn != (int)blockIdx.z) continue;
     const char* Ai = static_cast<const char*>(a.A) + (int64_t)id * a.K * a.r * 2;
     const brsrc ra = make_rsrc(Ai + k0 * a.r * 2, klen * a.r * 2);
     f32x4 acc[RG][NJ];
@@ -234,17 +278,25 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
     for (int m = 0; m < RG; ++m)
 #pragma unroll
       for (int t = 0; t < NJ; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
-#pragma unroll 2
-    for (int k = 0; k < (int)klen; k += 32) {
-      bf16x8 fa[NJ], fx[RG];
-      load_a_frags<NJ>(ra, (uint32_t)(k + 8 * g), a.r, c, fa);
+    for (int k = 0; k < (int)klen; k += 64) {
+      AFrags<NJ> fa[2];
+      u32x4 fx[2][RG];
 #pragma unroll
-      for (int m = 0; m < RG; ++m)
-        fx[m] = __builtin_bit_cast(bf16x8, buf_load16(rx, xrow[m] + (xrow[m] < 0x80000000u ? (uint32_t)(k + 8 * g) * 2 : 0u)));
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t kk = (uint32_t)(k + 32 * h + 8 * g);
+        fa[h].load(ra, kk, a.r, c);
 #pragma unroll
-      for (int m = 0; m < RG; ++m)
+        for (int m = 0; m < RG; ++m) fx[h][m] = buf_load16(rx, xrow[m] < 0x80000000u ? xrow[m] + kk * 2 : xrow[m]);
+      }
 #pragma unroll
-        for (int t = 0; t < NJ; ++t) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[t], fx[m], acc[m][t], 0, 0, 0);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int t = 0; t < NJ; ++t) {
+          const bf16x8 f = fa[h].frag(t);
+#pragma unroll
+          for (int m = 0; m < RG; ++m)
+            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, fx[h][m]), acc[m][t], 0, 0, 0);
+        }
     }
     // the four quarters of the K range, in ascending order
     if (w > 0)
@@ -256,14 +308,13 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
     if (w == 0) {
 #pragma unroll
       for (int m = 0; m < RG; ++m) {
-        const int64_t t = t0 + 16 * m + c;
+        float* u = a.upart + ((int64_t)kc * a.T + t0 + row[m]) * a.r;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
           f32x4 s = acc[m][j];
 #pragma unroll
           for (int q = 0; q < 3; ++q) s += red[q][m * NJ + j][lane];
           // rank index NJ (4 g + v) + j
-          float* u = a.upart + ((int64_t)kc * a.T + t) * a.r;
           if (rid[m] == id)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -277,11 +328,66 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
   }
 }
 
+// What the GEMM of many rows reads: blocks 0 .. ntile - 1 list the adapters of
+// their 256-row tile, the others sum U over its K ranges, scale it and round it
+// to bf16 (as the one-adapter calls do), 32 rows a block.
+__global__ __launch_bounds__(256) void multi_plan_kernel(const MultiArgs a) {
+  const int tiles = (int)((a.T + 255) / 256);
+  const int i = threadIdx.x;
+  if ((int)blockIdx.x < tiles) {
+    __shared__ int ids[256], firsts[256], blocks[256];
+    __shared__ int count;
+    MultiTile& p = a.plan[blockIdx.x];
+    const int id = row_id(a, (int64_t)blockIdx.x * 256 + i);
+    ids[i] = id;
+    blocks[i] = 0;
+    if (i == 0) count = 0;
+    __syncthreads();
+    bool first = id >= 0;
+#pragma unroll 8
+    for (int j = 0; j < 256; ++j) first = first && !(j < i && ids[j] == id);
+    firsts[i] = first ? id : 0x7fffffff;
+    __syncthreads();
+    int slot = 0;
+#pragma unroll 8
+    for (int j = 0; j < 256; ++j) slot += firsts[j] < id;
+    if (id >= 0) atomicOr(&blocks[slot], 1 << (i >> 4));
+    if (first) {
+      p.id[slot] = id;
+      atomicAdd(&count, 1);
+    }
+    p.slot[i] = id >= 0 ? slot : -1;
+    __syncthreads();
+    p.blocks[i] = (uint32_t)blocks[i];
+    if (i >= count) p.id[i] = 0;
+    if (i == 0) p.count = count;
+    return;
+  }
+  const int64_t t = ((int64_t)blockIdx.x - tiles) * 32 + (i >> 3);
+  const int j0 = (i & 7) * 8;
+  if (t >= a.T) return;
+  const int id = row_id(a, t);
+  u32x4 out = u32x4{0, 0, 0, 0};
+  if (id >= 0 && j0 < a.r) {  // the rank is a multiple of 8
+    f32x4 s0 = f32x4{0, 0, 0, 0}, s1 = s0;
+    for (int k = 0; k < a.kc; ++k) {
+      const f32x4* u = reinterpret_cast<const f32x4*>(a.upart + ((int64_t)k * a.T + t) * a.r + j0);
+      s0 += u[0];
+      s1 += u[1];
+    }
+    const float s = a.scales[id];
+    out = u32x4{pack_bf2(s * s0[0], s * s0[1]), pack_bf2(s * s0[2], s * s0[3]), pack_bf2(s * s1[0], s * s1[1]),
+                pack_bf2(s * s1[2], s * s1[3])};
+  }
+  *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) = out;
+}
+
 // ---------------------------------------------------------------------------
 // Y = sum of the K ranges' parts (or Y itself) + s_i U B_i, rounded once.
-// 16 rows a block, one wavefront per 4 rows and 512 columns: a lane owns 8
-// columns.  U of the block's rows is summed over its K ranges into LDS, times
-// the adapter's scale.  Four rows of one adapter share the loads of B_i.
+// A block has four rows and 64 C columns (a lane owns C of them); its four
+// wavefronts share the K parts and the ranks of all four rows, so that few
+// rows still have enough loads in flight, and meet in LDS, where wavefront w
+// adds them in ascending order for row w.
 // ---------------------------------------------------------------------------
 template <typename T>
 struct Cols;
@@ -300,79 +406,102 @@ struct Cols<uint16_t> {
     const u32x4 v = {pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]), pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7])};
     *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = v;
   }
+  static __device__ __forceinline__ void add(const float* p, float (&f)[8]) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(p), y = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      f[k] += x[k];
+      f[4 + k] += y[k];
+    }
+  }
 };
 template <>
 struct Cols<float> {
   static constexpr int N = 1;
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[1]) { f[0] = static_cast<const float*>(p)[i]; }
   static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[1]) { static_cast<float*>(p)[i] = f[0]; }
+  static __device__ __forceinline__ void add(const float* p, float (&f)[1]) { f[0] += p[0]; }
 };
 
 template <typename T>
 __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
   constexpr int C = Cols<T>::N;
-  __shared__ float us[16][64];
+  __shared__ float us[4][64];
+  __shared__ float sum[4][4][64 * C];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.y * 16;
-  const int64_t col = ((int64_t)blockIdx.x * 64 + lane) * C;
-  for (int e = threadIdx.x; e < 16 * a.r; e += 256) {
-    const int row = e / a.r, j = e % a.r;
-    const int64_t t = t0 + row;
-    const int id = row_id(a, t);
-    float s = 0.0f;
-    if (id >= 0) {
-      for (int k = 0; k < a.kc; ++k) s += a.upart[((int64_t)k * a.T + t) * a.r + j];
-      s *= a.scales[id];
-    }
-    us[row][j] = s;
-  }
-  __syncthreads();
-  if (col >= a.N) return;
-  float y[4][C];
+  const int cols = (int)((a.N + 64 * C - 1) / (64 * C));
+  const int64_t t0 = (int64_t)(blockIdx.x / cols) * 4;
+  const int64_t col = ((int64_t)(blockIdx.x % cols) * 64 + lane) * C;
+  const bool in = col < a.N;
+  const int rows = a.T - t0 < 4 ? (int)(a.T - t0) : 4;
   int id[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + 4 * w + i;
-    id[i] = __builtin_amdgcn_readfirstlane(row_id(a, t));
-    if (t >= a.T) continue;
+  for (int i = 0; i < 4; ++i) id[i] = __builtin_amdgcn_readfirstlane(row_id(a, t0 + i));
+  if (id[w] >= 0 && lane < a.r) {
+    float s = 0.0f;
+    const float* u = a.upart + (t0 + w) * a.r + lane;
+#pragma unroll 4
+    for (int k = 0; k < a.kc; ++k) s += u[(int64_t)k * a.T * a.r];
+    us[w][lane] = s * a.scales[id[w]];
+  }
+  float y[4][C];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < C; ++j) y[i][j] = 0.0f;
+  if (in) {
     if (a.part == nullptr) {
-      Cols<T>::load(a.Y, t * a.N + col, y[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i == w && i < rows) Cols<T>::load(a.Y, (t0 + i) * a.N + col, y[i]);
     } else {
+      const int64_t stride = a.T * a.N;
+      for (int k = w; k < a.ks; k += 4)
 #pragma unroll
-      for (int j = 0; j < C; ++j) y[i][j] = 0.0f;
-      for (int k = 0; k < a.ks; ++k) {
-        const float* p = a.part + ((int64_t)k * a.T + t) * a.N + col;
-#pragma unroll
-        for (int j = 0; j < C; ++j) y[i][j] += p[j];
-      }
+        for (int i = 0; i < 4; ++i)
+          if (i < rows) Cols<T>::add(a.part + k * stride + (t0 + i) * a.N + col, y[i]);
     }
   }
-  const int64_t bs = (int64_t)a.r * a.N;
-  if (id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
-    if (id[0] >= 0)
-      for (int j = 0; j < a.r; ++j) {
+  __syncthreads();
+  if (in) {
+    const int64_t bs = (int64_t)a.r * a.N;
+    auto rank = [&](int id_, int j, float (&b)[C]) { Cols<T>::load(a.B, id_ * bs + (int64_t)j * a.N + col, b); };
+    if (id[0] >= 0 && id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
+#pragma unroll 4
+      for (int j = w; j < a.r; j += 4) {
         float b[C];
-        Cols<T>::load(a.B, id[0] * bs + (int64_t)j * a.N + col, b);
+        rank(id[0], j, b);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int k = 0; k < C; ++k) y[i][k] = fmaf(us[4 * w + i][j], b[k], y[i][k]);
+          for (int k = 0; k < C; ++k) y[i][k] = fmaf(us[i][j], b[k], y[i][k]);
       }
-  } else {
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (id[i] < 0) continue;
-      for (int j = 0; j < a.r; ++j) {
-        float b[C];
-        Cols<T>::load(a.B, id[i] * bs + (int64_t)j * a.N + col, b);
+      for (int i = 0; i < 4; ++i) {
+        if (id[i] < 0) continue;
+#pragma unroll 4
+        for (int j = w; j < a.r; j += 4) {
+          float b[C];
+          rank(id[i], j, b);
 #pragma unroll
-        for (int k = 0; k < C; ++k) y[i][k] = fmaf(us[4 * w + i][j], b[k], y[i][k]);
+          for (int k = 0; k < C; ++k) y[i][k] = fmaf(us[i][j], b[k], y[i][k]);
+        }
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (t0 + 4 * w + i < a.T) Cols<T>::store(a.Y, (t0 + 4 * w + i) * a.N + col, y[i]);
+#pragma unroll
+    for (int j = 0; j < C; ++j) sum[w][i][j * 64 + lane] = y[i][j];
+  __syncthreads();
+  if (in && w < rows) {
+    float o[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      o[j] = sum[0][w][j * 64 + lane] + sum[1][w][j * 64 + lane] + sum[2][w][j * 64 + lane] + sum[3][w][j * 64 + lane];
+    Cols<T>::store(a.Y, (t0 + w) * a.N + col, o);
+  }
 }
 
 // U in fp32: one block per row; threads are (K slot, rank index), slots added in ascending order.
@@ -398,26 +527,55 @@ __global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
-// Row tiles of 32, 64 or 128: the smallest that hold all rows, 128 beyond.
-int row_tiles(int64_t T) { return T <= 32 ? 2 : T <= 64 ? 4 : 8; }
+// bf16 calls of up to kFewRows rows stream W in one row tile (16 rows and up)
+// and add the adapters to the fp32 sums; beyond that the 256 x 256 tiles of
+// the GEMM take over, with the adapters in its epilogue.
+constexpr int64_t kFewRows = 128;
 
-// K ranges of X W: enough blocks to fill the chip twice, each with at least
-// four K stages.
+// K ranges of X W for few rows, by a model of the grid: rounds of the blocks
+// that the chip holds, each as long as its K stages (16 KB of W at the CU's
+// share of HBM) and some 3 us to fill and drain, and the fp32 parts that are
+// written and read again.
 int base_ksplit(int64_t T, int64_t K, int64_t N) {
-  const int64_t units = cdiv(N, 128) * cdiv(T, 16 * row_tiles(T));
-  const int64_t want = cdiv(512, units), most = std::max<int64_t>(1, K / 256);
-  return (int)std::max<int64_t>(1, std::min(want, most));
+  const int mt = (int)cdiv(T, 16), per_cu = mt <= 5 ? 2 : 1;
+  const int64_t units = cdiv(N, 128), steps = K / 64;
+  double best = 0.0;
+  int bs = 1;
+  for (int s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
+    const double rounds = (double)cdiv(units * s, 256 * per_cu);
+    const double t = rounds * ((double)cdiv(steps, s) * 0.8 * per_cu + 3.0) + (double)s * T * N * 8 / 4e6;
+    if (s == 1 || t < best * 0.97) {
+      best = t;
+      bs = s;
+    }
+  }
+  return bs;
 }
 
 template <int MT>
 hipError_t launch_base(const MultiArgs& a, hipStream_t st) {
-  const int64_t nb = cdiv((int64_t)a.ntn * a.ks, 8) * 8 * a.ntm;
-  hipLaunchKernelGGL(multi_base_kernel<MT>, dim3((unsigned)nb), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(multi_base_kernel<MT>, dim3((unsigned)(a.ntn * a.ks)), dim3(256), 0, st, a);
   return hipGetLastError();
+}
+hipError_t launch_base_mt(const MultiArgs& a, hipStream_t st) {
+  switch (cdiv(a.T, 16)) {
+    case 1: return launch_base<1>(a, st);
+    case 2: return launch_base<2>(a, st);
+    case 3: return launch_base<3>(a, st);
+    case 4: return launch_base<4>(a, st);
+    case 5: return launch_base<5>(a, st);
+    case 6: return launch_base<6>(a, st);
+    case 7: return launch_base<7>(a, st);
+    default: return launch_base<8>(a, st);
+  }
 }
 template <int RG>
 hipError_t launch_shrink(const MultiArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)cdiv(a.T, 16 * RG), (unsigned)a.kc);
+  // 16 rows meet at most 16 adapters, each in a block of its own; of 64 sorted rows most meet one
+  // or two, and further blocks only fill the chip where there are few
+  const unsigned x = (unsigned)(RG == 4 ? 4 * cdiv(a.T, 256) : cdiv(a.T, 16));
+  const int64_t z = RG == 4 ? std::min<int64_t>(8, std::max<int64_t>(1, 1024 / ((int64_t)x * a.kc))) : 16;
+  const dim3 grid(x, (unsigned)a.kc, (unsigned)std::min(z, a.n));
   switch (cdiv(a.r, 16)) {
     case 1: hipLaunchKernelGGL((multi_shrink_kernel<RG, 1>), grid, dim3(256), 0, st, a); break;
     case 2: hipLaunchKernelGGL((multi_shrink_kernel<RG, 2>), grid, dim3(256), 0, st, a); break;
@@ -429,18 +587,26 @@ hipError_t launch_shrink(const MultiArgs& a, hipStream_t st) {
 
 // Workspace of a call.
 struct MultiPlan {
+  bool tiles;  // the GEMM path
   int ks, kc;
   float *part, *upart;
+  uint16_t* u;
+  MultiTile* plan;
   size_t bytes;
 };
 MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   MultiPlan p{};
   const bool bf16 = d.dtype == LORA_BF16;
-  p.ks = bf16 && base && d.T > 0 ? base_ksplit(d.T, d.K, d.N) : 1;
+  p.tiles = bf16 && base && d.T > kFewRows;
+  p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K) : base_ksplit(d.T, d.K, d.N);
   p.kc = bf16 ? (int)cdiv(d.K, kShrinkK) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
-  if (bf16 && base) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
+  if (p.tiles) {
+    p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
+    p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
+  }
+  if (bf16 && base && (!p.tiles || p.ks > 1)) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
   p.bytes = w.off;
   return p;
 }
@@ -522,16 +688,48 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   a.r = (int32_t)d->r;
   a.ks = p.ks;
   a.kc = p.kc;
-  const int mt = row_tiles(d->T);
   a.ntn = (int32_t)cdiv(d->N, 128);
-  a.ntm = (int32_t)cdiv(d->T, 16 * mt);
+  a.u = p.u;
+  a.plan = p.plan;
   if (bf16) {
-    if (d->n > 0) LAUNCHN("multi_shrink", st, d->T <= 64 ? launch_shrink<1>(a, st) : launch_shrink<4>(a, st));
-    if (W)
-      LAUNCHN("multi_base", st, mt == 2 ? launch_base<2>(a, st) : mt == 4 ? launch_base<4>(a, st) : launch_base<8>(a, st));
+    if (d->n > 0) LAUNCHN("multi_shrink", st, d->T <= kFewRows ? launch_shrink<1>(a, st) : launch_shrink<4>(a, st));
+    if (p.tiles) {
+      {
+        TraceScope ts("multi_plan", st);
+        hipLaunchKernelGGL(multi_plan_kernel, dim3((unsigned)(cdiv(d->T, 256) + cdiv(d->T, 32))), dim3(256), 0, st, a);
+        LAUNCH(hipGetLastError());
+      }
+      GemmArgs g{};
+      g.M = d->T;
+      g.nseg = 1;
+      g.nreg = 1;
+      g.epi = EPI_STORE;
+      g.bkind = B_NN;
+      g.group = 8;
+      g.seg[0].A = X;
+      g.seg[0].lda = d->K;
+      g.seg[0].K = d->K;
+      g.seg[0].b[0][0].p = W;
+      g.seg[0].b[0][0].ld = d->N;
+      g.reg[0].N = d->N;
+      g.reg[0].out = Y;
+      g.reg[0].ldo = d->N;
+      g.ntile_m = cdiv(d->T, gemm_tile_rows(true));
+      g.ntile_n = cdiv(d->N, gemm_tile_cols(true, false));
+      g.ksplit = p.ks;
+      g.ksplit_t0 = (int32_t)store_gemm_split_from(g.ntile_m * g.ntile_n, p.ks);
+      g.kpart = p.part;
+      g.mt_u = p.u;
+      g.mt_b = B;
+      g.mt_plan = p.plan;
+      g.mt_r = (int32_t)d->r;
+      LAUNCHN("gemm_nn_store_multi", st, launch_gemm_bf16(g, st));
+      if (p.ks > 1) LAUNCHN("ksplit_reduce", st, launch_ksplit_reduce(g, st));
+      return LORA_OK;
+    }
+    if (W) LAUNCHN("multi_base", st, launch_base_mt(a, st));
     TraceScope ts("multi_expand", st);
-    hipLaunchKernelGGL(multi_expand_kernel<uint16_t>, dim3((unsigned)cdiv(d->N, 512), (unsigned)cdiv(d->T, 16)), dim3(256), 0,
-                       st, a);
+    hipLaunchKernelGGL(multi_expand_kernel<uint16_t>, dim3((unsigned)(cdiv(d->N, 512) * cdiv(d->T, 4))), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
     return LORA_OK;
   }
@@ -562,7 +760,7 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
       LAUNCH(hipGetLastError());
     }
     TraceScope ts("multi_expand_f32", st);
-    hipLaunchKernelGGL(multi_expand_kernel<float>, dim3((unsigned)cdiv(d->N, 64), (unsigned)cdiv(d->T, 16)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(multi_expand_kernel<float>, dim3((unsigned)(cdiv(d->N, 64) * cdiv(d->T, 4))), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
   }
   return LORA_OK;
