@@ -176,18 +176,16 @@ __global__ __launch_bounds__(256) void multi_base_kernel(const MultiArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// U = X A_i (bf16): fp32 sums over K ranges of kShrinkK, for 16 RG rows a
-// block.  Every wavefront takes a quarter of the range for all of the rows
-// and walks the distinct adapters of the rows, each multiplied against all
-// of them (the MFMA computes 16 rows at a time anyway) and kept where it is
-// the row's own.  gridDim.z blocks share the walk.  With many rows (RG = 4)
-// the rows of a 256-row tile are first put in the order of their adapters, so
-// that 64 of them meet few.  A_i [K, r] is read as it lies: lane 16 q + c
-// takes columns NJ c .. NJ c + NJ - 1 of 8 consecutive K rows, which after a
-// transpose in registers are the operands of NJ tiles (tile t: rank index
-// NJ c + t).
+// U = X A_i for few rows (bf16): fp32 sums over K ranges of 1024.  A block has
+// 16 rows; its four wavefronts take 256 K each, hold X of them in registers,
+// and walk the distinct adapters of the rows, each multiplied against all of
+// them (the MFMA computes 16 rows at a time anyway) and kept where it is the
+// row's own; gridDim.z blocks share the walk, so that as a rule a block meets
+// one adapter.  A_i [K, r] is read as it lies: lane 16 q + c takes columns
+// NJ c .. NJ c + NJ - 1 of 8 consecutive K rows, which after a transpose in
+// registers are the operands of NJ tiles (tile t: rank index NJ c + t).
 // ---------------------------------------------------------------------------
-constexpr int kShrinkK = 1024;
+constexpr int kShrinkK = 256;  // per wavefront
 
 template <int NJ>
 struct AFrags {
@@ -224,158 +222,228 @@ struct AFrags {
   }
 };
 
-template <int RG, int NJ>
-__global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
-  __shared__ f32x4 red[3][RG * NJ][64];
+template <int NJ>
+__global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a) {
+  constexpr int STEPS = kShrinkK / 32;                           // K steps of a wavefront
+  constexpr int FLY = NJ == 3 ? 2 : NJ == 4 ? 4 : 8;             // of A_i, loaded at a time
+  __shared__ f32x4 red[3][NJ][64];
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
   const int kc = blockIdx.y;
-  const int64_t k0 = (int64_t)kc * kShrinkK + w * (kShrinkK / 4);
-  const int64_t klen = a.K - k0 < kShrinkK / 4 ? a.K - k0 : kShrinkK / 4;  // multiple of 64, may be <= 0
-  // row (relative to t0) and adapter of MFMA row `lane` (lane < 16 RG)
-  int64_t t0;
-  int my, myrow;
-  if constexpr (RG == 4) {
-    __shared__ int ids[256], row_of[256], id_of[256];
-    const int i = threadIdx.x;
-    t0 = (int64_t)(blockIdx.x >> 2) * 256;
-    const int id = row_id(a, t0 + i);
-    const int key = id < 0 ? 0x7fffffff : id;
-    ids[i] = key;
-    __syncthreads();
-    int rank = 0;
-#pragma unroll 8
-    for (int j = 0; j < 256; ++j) rank += ids[j] < key || (ids[j] == key && j < i);
-    row_of[rank] = i;
-    id_of[rank] = id;
-    __syncthreads();
-    myrow = row_of[64 * (blockIdx.x & 3) + lane];
-    my = id_of[64 * (blockIdx.x & 3) + lane];
-  } else {
-    t0 = (int64_t)blockIdx.x * (16 * RG);
-    myrow = lane & (16 * RG - 1);
-    my = lane < 16 * RG ? row_id(a, t0 + lane) : -1;
-  }
-  int rid[RG], row[RG];  // of this lane's MFMA rows
-  uint32_t xrow[RG];     // rows past T read zero
-#pragma unroll
-  for (int m = 0; m < RG; ++m) {
-    rid[m] = __shfl(my, 16 * m + c);
-    row[m] = __shfl(myrow, 16 * m + c);
-    xrow[m] = t0 + row[m] < a.T ? (uint32_t)(row[m] * a.K * 2) : 0x80000000u;
-  }
-  const brsrc rx = make_rsrc(static_cast<const char*>(a.X) + (t0 * a.K + k0) * 2, ((a.T - t0) * a.K - k0) * 2);
+  const int64_t k0 = (int64_t)(4 * kc + w) * kShrinkK;
+  const int64_t klen = a.K - k0 < kShrinkK ? a.K - k0 : kShrinkK;  // multiple of 64, may be <= 0
+  const int64_t t0 = (int64_t)blockIdx.x * 16;
+  const int my = lane < 16 ? row_id(a, t0 + lane) : -1;
   uint64_t todo = __ballot(my >= 0);
+  if (todo == 0) return;  // uniform over the block
+  const int rid = __shfl(my, c);  // adapter of the lane's MFMA row
+  const brsrc rx = make_rsrc(static_cast<const char*>(a.X) + (t0 * a.K + k0) * 2, ((a.T - t0) * a.K - k0) * 2);
+  u32x4 fx[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s)  // rows past T and K past the range read zero
+    fx[s] = buf_load16(rx, t0 + c < a.T && 32 * s < klen ? (uint32_t)((c * a.K + 32 * s + 8 * g) * 2) : 0x80000000u);
   for (int turn = 0; todo != 0; turn = turn + 1 == (int)gridDim.z ? 0 : turn + 1) {
     const int id = __builtin_amdgcn_readlane(my, __builtin_ctzll(todo));
     todo &= ~__ballot(my == id);
     if (turn != (int)blockIdx.z) continue;
     const char* Ai = static_cast<const char*>(a.A) + (int64_t)id * a.K * a.r * 2;
     const brsrc ra = make_rsrc(Ai + k0 * a.r * 2, klen * a.r * 2);
-    f32x4 acc[RG][NJ];
+    f32x4 acc[NJ];
 #pragma unroll
-    for (int m = 0; m < RG; ++m)
+    for (int t = 0; t < NJ; ++t) acc[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int t = 0; t < NJ; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
-    for (int k = 0; k < (int)klen; k += 64) {
-      AFrags<NJ> fa[2];
-      u32x4 fx[2][RG];
+    for (int s0 = 0; s0 < STEPS; s0 += FLY) {
+      AFrags<NJ> fa[FLY];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t kk = (uint32_t)(k + 32 * h + 8 * g);
-        fa[h].load(ra, kk, a.r, c);
+      for (int s = 0; s < FLY; ++s) fa[s].load(ra, (uint32_t)(32 * (s0 + s) + 8 * g), a.r, c);
 #pragma unroll
-        for (int m = 0; m < RG; ++m) fx[h][m] = buf_load16(rx, xrow[m] < 0x80000000u ? xrow[m] + kk * 2 : xrow[m]);
-      }
+      for (int s = 0; s < FLY; ++s)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < NJ; ++t) {
-          const bf16x8 f = fa[h].frag(t);
-#pragma unroll
-          for (int m = 0; m < RG; ++m)
-            acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, fx[h][m]), acc[m][t], 0, 0, 0);
-        }
+        for (int t = 0; t < NJ; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s].frag(t), __builtin_bit_cast(bf16x8, fx[s0 + s]), acc[t], 0, 0, 0);
     }
     // the four quarters of the K range, in ascending order
     if (w > 0)
 #pragma unroll
-      for (int m = 0; m < RG; ++m)
-#pragma unroll
-        for (int t = 0; t < NJ; ++t) red[w - 1][m * NJ + t][lane] = acc[m][t];
+      for (int t = 0; t < NJ; ++t) red[w - 1][t][lane] = acc[t];
     __syncthreads();
     if (w == 0) {
+      float* u = a.upart + ((int64_t)kc * a.T + t0 + c) * a.r;
 #pragma unroll
-      for (int m = 0; m < RG; ++m) {
-        float* u = a.upart + ((int64_t)kc * a.T + t0 + row[m]) * a.r;
+      for (int t = 0; t < NJ; ++t) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          f32x4 s = acc[m][j];
+        for (int q = 0; q < 3; ++q) acc[t] += red[q][t][lane];
+        if (rid == id)
 #pragma unroll
-          for (int q = 0; q < 3; ++q) s += red[q][m * NJ + j][lane];
-          // rank index NJ (4 g + v) + j
-          if (rid[m] == id)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int i = NJ * (4 * g + v) + j;
-              if (i < a.r) u[i] = s[v];
-            }
-        }
+          for (int v = 0; v < 4; ++v) {
+            const int i = NJ * (4 * g + v) + t;  // rank index
+            if (i < a.r) u[i] = acc[t][v];
+          }
       }
     }
     __syncthreads();
   }
 }
 
-// What the GEMM of many rows reads: blocks 0 .. ntile - 1 list the adapters of
-// their 256-row tile, the others sum U over its K ranges, scale it and round it
-// to bf16 (as the one-adapter calls do), 32 rows a block.
-__global__ __launch_bounds__(256) void multi_plan_kernel(const MultiArgs a) {
-  const int tiles = (int)((a.T + 255) / 256);
+// ---------------------------------------------------------------------------
+// U = X A_i for many rows (bf16): fp32 sums over K ranges of 256.  A block has
+// a 256-row tile, whose rows it first puts in the order of their adapters, and
+// a wavefront holds X of 64 of those, by 256 K, in registers: read once, all
+// loads in flight together.  The block then walks the tile's adapters: the
+// [256, r] slice of A_i, contiguous in memory, is copied to LDS one adapter
+// ahead and read with the transposing read (tile t: rank index 16 t + c), and
+// a wavefront multiplies it where its rows have that adapter.  The first
+// block of a tile also lists its adapters for the GEMM.  (Blocks of 32 or 64
+// rows, each sorting the tile for itself, took longer to sort than to read X,
+// and A_i by loads into registers left each adapter a chain of latencies.)
+// ---------------------------------------------------------------------------
+// Rows of a 256-row tile in the order of their adapters (rows without one
+// last), by 256 threads: id_of and row_of hold the sorted ids and rows.
+__device__ __forceinline__ void sort_tile(int id, int* keys, int* id_of, int* row_of) {
   const int i = threadIdx.x;
-  if ((int)blockIdx.x < tiles) {
-    __shared__ int ids[256], firsts[256], blocks[256];
-    __shared__ int count;
-    MultiTile& p = a.plan[blockIdx.x];
-    const int id = row_id(a, (int64_t)blockIdx.x * 256 + i);
-    ids[i] = id;
-    blocks[i] = 0;
-    if (i == 0) count = 0;
-    __syncthreads();
-    bool first = id >= 0;
-#pragma unroll 8
-    for (int j = 0; j < 256; ++j) first = first && !(j < i && ids[j] == id);
-    firsts[i] = first ? id : 0x7fffffff;
-    __syncthreads();
-    int slot = 0;
-#pragma unroll 8
-    for (int j = 0; j < 256; ++j) slot += firsts[j] < id;
-    if (id >= 0) atomicOr(&blocks[slot], 1 << (i >> 4));
-    if (first) {
-      p.id[slot] = id;
-      atomicAdd(&count, 1);
-    }
-    p.slot[i] = id >= 0 ? slot : -1;
-    __syncthreads();
-    p.blocks[i] = (uint32_t)blocks[i];
-    if (i >= count) p.id[i] = 0;
-    if (i == 0) p.count = count;
-    return;
+  const int key = id < 0 ? 0x7fffffff : id;
+  keys[i] = key;
+  __syncthreads();
+  int rank = 0;
+  const int4* k4 = reinterpret_cast<const int4*>(keys);
+#pragma unroll 16
+  for (int j = 0; j < 64; ++j) {
+    const int4 k = k4[j];
+    // equal keys keep their order
+    rank += (int)(k.x < key) + (int)(k.y < key) + (int)(k.z < key) + (int)(k.w < key);
+    rank += ((int)(k.x == key) & (int)(4 * j < i)) + ((int)(k.y == key) & (int)(4 * j + 1 < i)) +
+            ((int)(k.z == key) & (int)(4 * j + 2 < i)) + ((int)(k.w == key) & (int)(4 * j + 3 < i));
   }
-  const int64_t t = ((int64_t)blockIdx.x - tiles) * 32 + (i >> 3);
-  const int j0 = (i & 7) * 8;
+  id_of[rank] = id;
+  row_of[rank] = i;
+  __syncthreads();
+}
+
+// Slots of a sorted tile: `slot` of this thread's row (-1: none), the adapter
+// of each slot in ids, and their number.
+__device__ __forceinline__ void slots_of_tile(const int* id_of, int* heads, int* ids, int& slot, int& count) {
+  const int i = threadIdx.x, lane = i & 63, w = i >> 6;
+  const int id = id_of[i];
+  const bool first = id >= 0 && (i == 0 || id_of[i - 1] != id);
+  const uint64_t m = __ballot(first);
+  if (lane == 0) heads[w] = __popcll(m);
+  __syncthreads();
+  int n = __popcll(m & ((2ull << lane) - 1)) - 1;  // firsts up to here, in this wavefront and those before
+  for (int k = 0; k < w; ++k) n += heads[k];
+  if (first) ids[n] = id;
+  slot = id >= 0 ? n : -1;
+  count = __builtin_amdgcn_readfirstlane(heads[0] + heads[1] + heads[2] + heads[3]);
+  __syncthreads();
+}
+
+// The GEMM's list of the tile (blocks: 256 ints).
+__device__ __forceinline__ void list_tile(MultiTile& p, const int* id_of, const int* row_of, const int* ids, int slot,
+                                          int count, int* blocks) {
+  const int i = threadIdx.x;
+  blocks[i] = 0;
+  __syncthreads();
+  if (slot >= 0) atomicOr(&blocks[slot], 1 << (row_of[i] >> 4));
+  p.slot[row_of[i]] = slot;
+  p.id[i] = i < count ? ids[i] : 0;
+  if (i == 0) p.count = count;
+  __syncthreads();
+  p.blocks[i] = (uint32_t)blocks[i];
+}
+
+template <int NJ>
+__global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
+  constexpr int RG = 4, STEPS = kShrinkK / 32;
+  constexpr int SLICE = kShrinkK * NJ * 32 + 128;  // bytes of a slice; fragments of the last row may reach past it
+  __shared__ __attribute__((aligned(1024))) char slices[2 * SLICE];
+  __shared__ __attribute__((aligned(16))) int keys[256];
+  __shared__ int id_of[256], row_of[256], heads[4], ids[256];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int kc = blockIdx.y;
+  const int64_t k0 = (int64_t)kc * kShrinkK;
+  const int64_t klen = a.K - k0 < kShrinkK ? a.K - k0 : kShrinkK;  // multiple of 64
+  const int64_t t0 = (int64_t)blockIdx.x * 256;
+  int slot, count;
+  sort_tile(row_id(a, t0 + threadIdx.x), keys, id_of, row_of);
+  slots_of_tile(id_of, heads, ids, slot, count);
+  if (kc == 0 && blockIdx.z == 0) list_tile(a.plan[blockIdx.x], id_of, row_of, ids, slot, count, keys);
+  const int first = blockIdx.z, every = gridDim.z;  // this block's share of the adapters
+  if (first >= count) return;                       // uniform over the block
+  lds_char* const lds = (lds_char*)slices;
+  auto issue = [&](int s, int buf) {
+    const int64_t id = __builtin_amdgcn_readfirstlane(ids[s]);
+    const i32x4 ra = rsrc_words(static_cast<const char*>(a.A) + (id * a.K + k0) * a.r * 2, klen * a.r * 2);
+    for (int b = w; b < a.r / 2; b += 4)  // 1 KB each
+      dma16(ra, (uint32_t)(b * 1024 + lane * 16), lds_addr(lds) + buf * SLICE + b * 1024);
+  };
+  const int my = slot, myrow = row_of[threadIdx.x];
+  const brsrc rx = make_rsrc(static_cast<const char*>(a.X) + (t0 * a.K + k0) * 2, ((a.T - t0) * a.K - k0) * 2);
+  int rslot[RG], row[RG];  // of this lane's MFMA rows
+  u32x4 fx[RG][STEPS];
+  const bool any = __ballot(my >= 0) != 0;
+#pragma unroll
+  for (int m = 0; m < RG; ++m) {
+    rslot[m] = __shfl(my, 16 * m + c);
+    row[m] = __shfl(myrow, 16 * m + c);
+    const uint32_t at = (uint32_t)(row[m] * a.K * 2);
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s)  // rows past T or without an adapter and K past the range read zero
+      fx[m][s] = buf_load16(rx, any && rslot[m] >= 0 && 32 * s < klen ? at + (uint32_t)(32 * s + 8 * g) * 2 : 0x80000000u);
+  }
+  issue(first, 0);
+  int buf = 0;
+  for (int s = first; s < count; s += every, buf ^= 1) {
+    wait_vmcnt<0>();
+    __syncthreads();  // slice s is in for every wavefront, and the one before is no longer read
+    if (s + every < count) issue(s + every, buf ^ 1);
+    if (__ballot(my == s) == 0) continue;  // no row of this wavefront
+    f32x4 acc[RG][NJ];
+#pragma unroll
+    for (int m = 0; m < RG; ++m)
+#pragma unroll
+      for (int t = 0; t < NJ; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
+    const uint32_t ld = (uint32_t)a.r * 2;
+    const lds_char* const at = lds + buf * SLICE + (8 * g + (c >> 2)) * ld + (lane & 3) * 8;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k)
+#pragma unroll
+      for (int t = 0; t < NJ; ++t) {
+        const bf16x8 f = lds_read_tr8(at + 32 * k * ld + 32 * t, (int)(4 * ld));
+#pragma unroll
+        for (int m = 0; m < RG; ++m)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, __builtin_bit_cast(bf16x8, fx[m][k]), acc[m][t], 0, 0, 0);
+      }
+#pragma unroll
+    for (int m = 0; m < RG; ++m) {
+      float* u = a.upart + ((int64_t)kc * a.T + t0 + row[m]) * a.r + 4 * g;
+      if (rslot[m] == s)
+#pragma unroll
+        for (int t = 0; t < NJ; ++t)  // rank indices 16 t + 4 g .. + 3 (the rank is a multiple of 8)
+          if (16 * t + 4 * g < a.r) *reinterpret_cast<f32x4*>(u + 16 * t) = acc[m][t];
+    }
+  }
+}
+
+// U of many rows as the GEMM reads it: summed over the K ranges, scaled and
+// rounded to bf16 (as the one-adapter calls do), 32 rows a block.
+__global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
+  const int64_t t = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
+  const int j0 = (threadIdx.x & 7) * 8;
   if (t >= a.T) return;
   const int id = row_id(a, t);
   u32x4 out = u32x4{0, 0, 0, 0};
   if (id >= 0 && j0 < a.r) {  // the rank is a multiple of 8
     f32x4 s0 = f32x4{0, 0, 0, 0}, s1 = s0;
-    for (int k = 0; k < a.kc; ++k) {
-      const f32x4* u = reinterpret_cast<const f32x4*>(a.upart + ((int64_t)k * a.T + t) * a.r + j0);
-      s0 += u[0];
-      s1 += u[1];
-    }
+    const float* u = a.upart + t * a.r + j0;
     const float s = a.scales[id];
+#pragma unroll 8
+    for (int k = 0; k < a.kc; ++k) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(u + (int64_t)k * a.T * a.r);
+      s0 += p[0];
+      s1 += p[1];
+    }
     out = u32x4{pack_bf2(s * s0[0], s * s0[1]), pack_bf2(s * s0[2], s * s0[3]), pack_bf2(s * s1[0], s * s1[1]),
                 pack_bf2(s * s1[2], s * s1[3])};
   }
@@ -569,19 +637,27 @@ hipError_t launch_base_mt(const MultiArgs& a, hipStream_t st) {
     default: return launch_base<8>(a, st);
   }
 }
-template <int RG>
+// K ranges of the shrink.
+int shrink_ranges(int64_t T, int64_t K) { return (int)cdiv(K, T > kFewRows ? kShrinkK : 4 * kShrinkK); }
+
+// Few rows: 16 of them meet at most 16 adapters, each in a block of its own.
+// Many: two blocks share the adapters of a tile where the grid leaves room.
 hipError_t launch_shrink(const MultiArgs& a, hipStream_t st) {
-  // 16 rows meet at most 16 adapters, each in a block of its own; of 64 sorted rows most meet one
-  // or two, and further blocks only fill the chip where there are few
-  const unsigned x = (unsigned)(RG == 4 ? 4 * cdiv(a.T, 256) : cdiv(a.T, 16));
-  const int64_t z = RG == 4 ? std::min<int64_t>(8, std::max<int64_t>(1, 1024 / ((int64_t)x * a.kc))) : 16;
-  const dim3 grid(x, (unsigned)a.kc, (unsigned)std::min(z, a.n));
+  const bool many = a.T > kFewRows;
+  const int64_t x = cdiv(a.T, many ? 256 : 16), z = !many ? 16 : x * a.kc < 512 ? 2 : 1;
+  const dim3 grid((unsigned)x, (unsigned)a.kc, (unsigned)std::max<int64_t>(1, std::min(z, a.n)));
+#define LORA_SHRINK(NJ)                                                                            \
+  case NJ:                                                                                         \
+    if (many) hipLaunchKernelGGL(multi_shrink_kernel<NJ>, grid, dim3(256), 0, st, a);              \
+    else hipLaunchKernelGGL(multi_shrink_few_kernel<NJ>, grid, dim3(256), 0, st, a);               \
+    break
   switch (cdiv(a.r, 16)) {
-    case 1: hipLaunchKernelGGL((multi_shrink_kernel<RG, 1>), grid, dim3(256), 0, st, a); break;
-    case 2: hipLaunchKernelGGL((multi_shrink_kernel<RG, 2>), grid, dim3(256), 0, st, a); break;
-    case 3: hipLaunchKernelGGL((multi_shrink_kernel<RG, 3>), grid, dim3(256), 0, st, a); break;
-    default: hipLaunchKernelGGL((multi_shrink_kernel<RG, 4>), grid, dim3(256), 0, st, a); break;
+    LORA_SHRINK(1);
+    LORA_SHRINK(2);
+    LORA_SHRINK(3);
+    LORA_SHRINK(4);
   }
+#undef LORA_SHRINK
   return hipGetLastError();
 }
 
@@ -599,11 +675,11 @@ MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   const bool bf16 = d.dtype == LORA_BF16;
   p.tiles = bf16 && base && d.T > kFewRows;
   p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K) : base_ksplit(d.T, d.K, d.N);
-  p.kc = bf16 ? (int)cdiv(d.K, kShrinkK) : 1;
+  p.kc = bf16 ? shrink_ranges(d.T, d.K) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
-  if (p.tiles) {
-    p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
+  if (p.tiles) p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
+  if (bf16 && d.T > kFewRows) {
     p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
   }
   if (bf16 && base && (!p.tiles || p.ks > 1)) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
@@ -692,11 +768,12 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   a.u = p.u;
   a.plan = p.plan;
   if (bf16) {
-    if (d->n > 0) LAUNCHN("multi_shrink", st, d->T <= kFewRows ? launch_shrink<1>(a, st) : launch_shrink<4>(a, st));
+    // without adapters the shrink still lists the (empty) tiles of the GEMM
+    if (p.tiles || d->n > 0) LAUNCHN("multi_shrink", st, launch_shrink(a, st));
     if (p.tiles) {
       {
-        TraceScope ts("multi_plan", st);
-        hipLaunchKernelGGL(multi_plan_kernel, dim3((unsigned)(cdiv(d->T, 256) + cdiv(d->T, 32))), dim3(256), 0, st, a);
+        TraceScope ts("multi_u", st);
+        hipLaunchKernelGGL(multi_u_kernel, dim3((unsigned)cdiv(d->T, 32)), dim3(256), 0, st, a);
         LAUNCH(hipGetLastError());
       }
       GemmArgs g{};
