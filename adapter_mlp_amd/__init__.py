@@ -11,7 +11,9 @@ adapters select the fp32 LoRA-gradient mode (fp32 dA, dB).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -33,10 +35,16 @@ load = L.load
 LoraError = L.LoraError
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -109,14 +117,15 @@ def _set_plan(desc, plan):
     return desc
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
 def _on(stream):
     """Allocation context of a call: PyTorch's caching allocator ties every
     tensor allocated inside it (outputs, workspace) to the stream the library
     enqueues on, so a buffer is not handed to other work while the call's
     kernels may still use it."""
-    import contextlib
-
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+    return _NO_STREAM if stream is None else _torch().cuda.stream(stream)
 
 
 def _need(name, t, shape, dtype, device):
@@ -124,7 +133,7 @@ def _need(name, t, shape, dtype, device):
     this device (the kernels take row-major dense buffers)."""
     if t is None:
         raise ValueError(f"{name} is missing")
-    if tuple(t.shape) != tuple(int(x) for x in shape):
+    if t.shape != shape and tuple(t.shape) != tuple(int(x) for x in shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(int(x) for x in shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -597,14 +606,16 @@ def _call_on(t, stream, name, *args):
     torch = _torch()
     dev = t.device
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)  # torch.cuda.current_stream(dev).cuda_stream, without the object
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
+    else:
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        L.call(name, *args, stream.cuda_stream)
+        L.call(name, *args, raw)
     else:
         with torch.cuda.device(dev):
-            L.call(name, *args, stream.cuda_stream)
+            L.call(name, *args, raw)
 
 
 @dataclass
@@ -616,6 +627,7 @@ class AdapterPool:
     scale: object
 
 
+@functools.lru_cache(maxsize=1024)
 def multi_workspace_size(T, K, N, r, n, dtype=L.LORA_BF16):
     d = L.lora_multi_desc(T, K, N, r, n, dtype, 0)
     b = C.c_size_t()
@@ -692,6 +704,7 @@ def _norm_call(R, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_off
     return L.lora_norm_desc(T, H, eps, res_scale, branch_scale, int(unit_offset), kind, dt, 0)
 
 
+@functools.lru_cache(maxsize=1024)
 def block_norm_workspace_size(T, H, dtype=L.LORA_BF16):
     """Bytes of the backward's workspace (the forward takes none)."""
     d = L.lora_norm_desc(T, H, 0.0, 1.0, 1.0, 0, L.LORA_GATE_NONE, dtype, 0)

@@ -185,7 +185,7 @@ def load(path: str = LIB_PATH) -> C.CDLL:
 
 def call(name: str, *args) -> None:
     """Call a status-returning entry point; raise LoraError on failure."""
-    lib = load()
+    lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != LORA_OK:
         raise LoraError(name, st, lib.lora_last_error().decode())

@@ -20,6 +20,7 @@ struct MultiArgs {
   float* upart;  // [kc, T, r] fp32 sums of X A_i over K ranges
   int64_t T, K, N, n;
   int32_t r, ks, kc, ntn;
+  int32_t nshrink, nz;  // few rows: blocks of the shrink, and how many share the adapters of 16 rows
   uint16_t* u;       // [T, 64] bf16: scaled U, zero past the rank (many rows)
   MultiTile* plan;   // adapters of every 256-row tile (many rows)
 };
@@ -169,12 +170,6 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
   }
 }
 
-template <int MT>
-__global__ __launch_bounds__(256) void multi_base_kernel(const MultiArgs a) {
-  __shared__ __attribute__((aligned(1024))) char ring[BaseCfg<MT>::SMEM];
-  base_block<MT>(a, ring, blockIdx.x);
-}
-
 // ---------------------------------------------------------------------------
 // U = X A_i for few rows (bf16): fp32 sums over K ranges of 1024.  A block has
 // 16 rows; its four wavefronts take 256 K each, hold X of them in registers,
@@ -223,17 +218,16 @@ struct AFrags {
 };
 
 template <int NJ>
-__global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a) {
-  constexpr int STEPS = kShrinkK / 32;                           // K steps of a wavefront
-  constexpr int FLY = NJ == 3 ? 2 : NJ == 4 ? 4 : 8;             // of A_i, loaded at a time
-  __shared__ f32x4 red[3][NJ][64];
+__device__ __forceinline__ void shrink_few_block(const MultiArgs& a, char* lds, int bx, int kc, int bz, int nz) {
+  constexpr int STEPS = kShrinkK / 32;                // K steps of a wavefront
+  constexpr int FLY = NJ == 3 ? 2 : NJ == 4 ? 4 : 8;  // of A_i, loaded at a time
+  f32x4(*red)[NJ][64] = reinterpret_cast<f32x4(*)[NJ][64]>(lds);
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, c = lane & 15;
-  const int kc = blockIdx.y;
   const int64_t k0 = (int64_t)(4 * kc + w) * kShrinkK;
   const int64_t klen = a.K - k0 < kShrinkK ? a.K - k0 : kShrinkK;  // multiple of 64, may be <= 0
-  const int64_t t0 = (int64_t)blockIdx.x * 16;
+  const int64_t t0 = (int64_t)bx * 16;
   const int my = lane < 16 ? row_id(a, t0 + lane) : -1;
   uint64_t todo = __ballot(my >= 0);
   if (todo == 0) return;  // uniform over the block
@@ -243,10 +237,10 @@ __global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a
 #pragma unroll
   for (int s = 0; s < STEPS; ++s)  // rows past T and K past the range read zero
     fx[s] = buf_load16(rx, t0 + c < a.T && 32 * s < klen ? (uint32_t)((c * a.K + 32 * s + 8 * g) * 2) : 0x80000000u);
-  for (int turn = 0; todo != 0; turn = turn + 1 == (int)gridDim.z ? 0 : turn + 1) {
+  for (int turn = 0; todo != 0; turn = turn + 1 == nz ? 0 : turn + 1) {
     const int id = __builtin_amdgcn_readlane(my, __builtin_ctzll(todo));
     todo &= ~__ballot(my == id);
-    if (turn != (int)blockIdx.z) continue;
+    if (turn != bz) continue;
     const char* Ai = static_cast<const char*>(a.A) + (int64_t)id * a.K * a.r * 2;
     const brsrc ra = make_rsrc(Ai + k0 * a.r * 2, klen * a.r * 2);
     f32x4 acc[NJ];
@@ -284,6 +278,26 @@ __global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a
     }
     __syncthreads();
   }
+}
+
+// Both in one launch, which neither waits for the other in: blocks 0 ..
+// nshrink - 1 form U (first, since they are short), the rest X W.
+template <int MT>
+__global__ __launch_bounds__(256, BaseCfg<MT>::PER_CU) void multi_few_kernel(const MultiArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[BaseCfg<MT>::SMEM];
+  static_assert(BaseCfg<MT>::SMEM >= 3 * 4 * 1024, "the shrink's exchange");
+  const int b = blockIdx.x;
+  if (b < a.nshrink) {
+    const int bx = b / (a.kc * a.nz), kz = b % (a.kc * a.nz);
+    switch ((a.r + 15) / 16) {
+      case 1: shrink_few_block<1>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+      case 2: shrink_few_block<2>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+      case 3: shrink_few_block<3>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+      default: shrink_few_block<4>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+    }
+    return;
+  }
+  base_block<MT>(a, lds, b - a.nshrink);
 }
 
 // ---------------------------------------------------------------------------
@@ -600,18 +614,28 @@ __global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a
 // the GEMM take over, with the adapters in its epilogue.
 constexpr int64_t kFewRows = 128;
 
+// K ranges of the shrink.
+int shrink_ranges(int64_t T, int64_t K) { return (int)cdiv(K, T > kFewRows ? kShrinkK : 4 * kShrinkK); }
+// Few rows: 16 of them meet at most 16 adapters, each in a block of its own.
+int shrink_share(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(16, n)); }
+int shrink_blocks(int64_t T, int64_t K, int64_t n) {
+  return n == 0 ? 0 : (int)cdiv(T, 16) * shrink_ranges(T, K) * shrink_share(n);
+}
+
 // K ranges of X W for few rows, by a model of the grid: rounds of the blocks
 // that the chip holds, each as long as its K stages (16 KB of W at the CU's
-// share of HBM) and some 3 us to fill and drain, and the fp32 parts that are
-// written and read again.
-int base_ksplit(int64_t T, int64_t K, int64_t N) {
+// share of HBM) and some 3 us to fill and drain, the fp32 parts that are
+// written and read again, and the shrink's 4 us where its blocks find no room
+// beside the others.
+int base_ksplit(int64_t T, int64_t K, int64_t N, int shrink) {
   const int mt = (int)cdiv(T, 16), per_cu = mt <= 5 ? 2 : 1;
   const int64_t units = cdiv(N, 128), steps = K / 64;
   double best = 0.0;
   int bs = 1;
   for (int s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
     const double rounds = (double)cdiv(units * s, 256 * per_cu);
-    const double t = rounds * ((double)cdiv(steps, s) * 0.8 * per_cu + 3.0) + (double)s * T * N * 8 / 4e6;
+    const double t = rounds * ((double)cdiv(steps, s) * 0.8 * per_cu + 3.0) + (double)s * T * N * 8 / 4e6 +
+                     (units * s + shrink > 256 * per_cu ? 4.0 : 0.0);
     if (s == 1 || t < best * 0.97) {
       best = t;
       bs = s;
@@ -621,43 +645,34 @@ int base_ksplit(int64_t T, int64_t K, int64_t N) {
 }
 
 template <int MT>
-hipError_t launch_base(const MultiArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(multi_base_kernel<MT>, dim3((unsigned)(a.ntn * a.ks)), dim3(256), 0, st, a);
+hipError_t launch_few(const MultiArgs& a, hipStream_t st) {
+  const int blocks = a.nshrink + (a.W ? a.ntn * a.ks : 0);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(multi_few_kernel<MT>, dim3((unsigned)blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
-hipError_t launch_base_mt(const MultiArgs& a, hipStream_t st) {
+hipError_t launch_few_mt(const MultiArgs& a, hipStream_t st) {
   switch (cdiv(a.T, 16)) {
-    case 1: return launch_base<1>(a, st);
-    case 2: return launch_base<2>(a, st);
-    case 3: return launch_base<3>(a, st);
-    case 4: return launch_base<4>(a, st);
-    case 5: return launch_base<5>(a, st);
-    case 6: return launch_base<6>(a, st);
-    case 7: return launch_base<7>(a, st);
-    default: return launch_base<8>(a, st);
+    case 1: return launch_few<1>(a, st);
+    case 2: return launch_few<2>(a, st);
+    case 3: return launch_few<3>(a, st);
+    case 4: return launch_few<4>(a, st);
+    case 5: return launch_few<5>(a, st);
+    case 6: return launch_few<6>(a, st);
+    case 7: return launch_few<7>(a, st);
+    default: return launch_few<8>(a, st);
   }
 }
-// K ranges of the shrink.
-int shrink_ranges(int64_t T, int64_t K) { return (int)cdiv(K, T > kFewRows ? kShrinkK : 4 * kShrinkK); }
-
-// Few rows: 16 of them meet at most 16 adapters, each in a block of its own.
-// Many: two blocks share the adapters of a tile where the grid leaves room.
+// Two blocks share the adapters of a tile where the grid leaves room.
 hipError_t launch_shrink(const MultiArgs& a, hipStream_t st) {
-  const bool many = a.T > kFewRows;
-  const int64_t x = cdiv(a.T, many ? 256 : 16), z = !many ? 16 : x * a.kc < 512 ? 2 : 1;
-  const dim3 grid((unsigned)x, (unsigned)a.kc, (unsigned)std::max<int64_t>(1, std::min(z, a.n)));
-#define LORA_SHRINK(NJ)                                                                            \
-  case NJ:                                                                                         \
-    if (many) hipLaunchKernelGGL(multi_shrink_kernel<NJ>, grid, dim3(256), 0, st, a);              \
-    else hipLaunchKernelGGL(multi_shrink_few_kernel<NJ>, grid, dim3(256), 0, st, a);               \
-    break
+  const int64_t x = cdiv(a.T, 256);
+  const dim3 grid((unsigned)x, (unsigned)a.kc, x * a.kc < 512 && a.n > 1 ? 2 : 1);
   switch (cdiv(a.r, 16)) {
-    LORA_SHRINK(1);
-    LORA_SHRINK(2);
-    LORA_SHRINK(3);
-    LORA_SHRINK(4);
+    case 1: hipLaunchKernelGGL(multi_shrink_kernel<1>, grid, dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL(multi_shrink_kernel<2>, grid, dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL(multi_shrink_kernel<3>, grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL(multi_shrink_kernel<4>, grid, dim3(256), 0, st, a); break;
   }
-#undef LORA_SHRINK
   return hipGetLastError();
 }
 
@@ -674,7 +689,8 @@ MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   MultiPlan p{};
   const bool bf16 = d.dtype == LORA_BF16;
   p.tiles = bf16 && base && d.T > kFewRows;
-  p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K) : base_ksplit(d.T, d.K, d.N);
+  p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K)
+                                              : base_ksplit(d.T, d.K, d.N, shrink_blocks(d.T, d.K, d.n));
   p.kc = bf16 ? shrink_ranges(d.T, d.K) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
@@ -768,8 +784,13 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   a.u = p.u;
   a.plan = p.plan;
   if (bf16) {
-    // without adapters the shrink still lists the (empty) tiles of the GEMM
-    if (p.tiles || d->n > 0) LAUNCHN("multi_shrink", st, launch_shrink(a, st));
+    if (d->T <= kFewRows) {
+      a.nz = shrink_share(d->n);
+      a.nshrink = shrink_blocks(d->T, d->K, d->n);
+      LAUNCHN("multi_few", st, launch_few_mt(a, st));
+    } else if (p.tiles || d->n > 0) {  // without adapters the GEMM's tiles are still listed, as empty
+      LAUNCHN("multi_shrink", st, launch_shrink(a, st));
+    }
     if (p.tiles) {
       {
         TraceScope ts("multi_u", st);
@@ -804,7 +825,6 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
       if (p.ks > 1) LAUNCHN("ksplit_reduce", st, launch_ksplit_reduce(g, st));
       return LORA_OK;
     }
-    if (W) LAUNCHN("multi_base", st, launch_base_mt(a, st));
     TraceScope ts("multi_expand", st);
     hipLaunchKernelGGL(multi_expand_kernel<uint16_t>, dim3((unsigned)(cdiv(d->N, 512) * cdiv(d->T, 4))), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
