@@ -466,16 +466,13 @@ __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
 
 // ---------------------------------------------------------------------------
 // Y = sum of the K ranges' parts (or Y itself) + s_i U B_i, rounded once.
-// A block has four rows and 64 C columns (a lane owns C of them); its four
+// A block has four rows and 512 columns (a lane owns 8 of them); its four
 // wavefronts share the K parts and the ranks of all four rows, so that few
 // rows still have enough loads in flight, and meet in LDS, where wavefront w
 // adds them in ascending order for row w.
 // ---------------------------------------------------------------------------
-template <typename T>
-struct Cols;
-template <>
-struct Cols<uint16_t> {
-  static constexpr int N = 8;
+// Eight columns of a row.
+struct Cols {
   static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[8]) {
     const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
@@ -497,17 +494,8 @@ struct Cols<uint16_t> {
     }
   }
 };
-template <>
-struct Cols<float> {
-  static constexpr int N = 1;
-  static __device__ __forceinline__ void load(const void* p, int64_t i, float (&f)[1]) { f[0] = static_cast<const float*>(p)[i]; }
-  static __device__ __forceinline__ void store(void* p, int64_t i, const float (&f)[1]) { static_cast<float*>(p)[i] = f[0]; }
-  static __device__ __forceinline__ void add(const float* p, float (&f)[1]) { f[0] += p[0]; }
-};
-
-template <typename T>
 __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
-  constexpr int C = Cols<T>::N;
+  constexpr int C = 8;
   __shared__ float us[4][64];
   __shared__ float sum[4][4][64 * C];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
@@ -535,19 +523,19 @@ __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
     if (a.part == nullptr) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (i == w && i < rows) Cols<T>::load(a.Y, (t0 + i) * a.N + col, y[i]);
+        if (i == w && i < rows) Cols::load(a.Y, (t0 + i) * a.N + col, y[i]);
     } else {
       const int64_t stride = a.T * a.N;
       for (int k = w; k < a.ks; k += 4)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (i < rows) Cols<T>::add(a.part + k * stride + (t0 + i) * a.N + col, y[i]);
+          if (i < rows) Cols::add(a.part + k * stride + (t0 + i) * a.N + col, y[i]);
     }
   }
   __syncthreads();
   if (in) {
     const int64_t bs = (int64_t)a.r * a.N;
-    auto rank = [&](int id_, int j, float (&b)[C]) { Cols<T>::load(a.B, id_ * bs + (int64_t)j * a.N + col, b); };
+    auto rank = [&](int id_, int j, float (&b)[C]) { Cols::load(a.B, id_ * bs + (int64_t)j * a.N + col, b); };
     if (id[0] >= 0 && id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
 #pragma unroll 4
       for (int j = w; j < a.r; j += 4) {
@@ -582,7 +570,7 @@ __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
 #pragma unroll
     for (int j = 0; j < C; ++j)
       o[j] = sum[0][w][j * 64 + lane] + sum[1][w][j * 64 + lane] + sum[2][w][j * 64 + lane] + sum[3][w][j * 64 + lane];
-    Cols<T>::store(a.Y, (t0 + w) * a.N + col, o);
+    Cols::store(a.Y, (t0 + w) * a.N + col, o);
   }
 }
 
@@ -603,6 +591,129 @@ __global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a
   if (slot == 0) {
     for (int q = 1; q < slots; ++q) s += red[q * a.r + j];
     a.upart[t * a.r + j] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Y in fp32: v_mfma_f32_16x16x4 straight from global memory, 32 x 32 outputs a
+// wavefront, any widths.  A step is 16 K: lane 16 q + c holds K 4 q .. 4 q + 3
+// of row c (X, one 16-byte load) and of column c (W), and gives one of the
+// four to each MFMA, which takes any K as long as both operands agree.
+//   KSPLIT: the block is one 32 x 32 tile and its wavefronts quarter K: few
+//   tiles still fill the chip, and the chain of loads is a quarter as long.
+//   Else 64 x 64 a block, a quadrant a wavefront: half the traffic.
+// The adapter's term joins in the epilogue, from U of the tile's rows in LDS.
+// ---------------------------------------------------------------------------
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+template <bool KSPLIT>
+__global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
+  constexpr int TILE = KSPLIT ? 32 : 64;
+  __shared__ f32x4 red[KSPLIT ? 4 : 1][KSPLIT ? 4 : 1][64];
+  __shared__ float us[TILE][65];
+  __shared__ int ids[TILE];
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, c = lane & 15;
+  const int tiles_n = (int)((a.N + TILE - 1) / TILE);
+  const int64_t mt = (int64_t)(blockIdx.x / tiles_n) * TILE, nt = (int64_t)(blockIdx.x % tiles_n) * TILE;
+  const int64_t m0 = KSPLIT ? mt : mt + 32 * (w & 1), n0 = KSPLIT ? nt : nt + 32 * (w >> 1);
+  for (int i = threadIdx.x; i < TILE; i += 256) ids[i] = row_id(a, mt + i);
+  __syncthreads();
+  for (int e = threadIdx.x; e < TILE * a.r; e += 256) {
+    const int row = e / a.r, j = e % a.r, id = ids[row];
+    us[row][j] = id >= 0 ? a.upart[(mt + row) * a.r + j] * a.scales[id] : 0.0f;
+  }
+  f32x4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  if (a.W != nullptr) {
+    const int64_t quarter = (a.K + 63) / 64 * 16;
+    const int64_t k0 = KSPLIT ? w * quarter : 0;
+    const int64_t k1 = KSPLIT && k0 + quarter < a.K ? k0 + quarter : a.K;
+    const float *X = static_cast<const float*>(a.X), *W = static_cast<const float*>(a.W);
+    float x[2][2][4], wv[2][2][4];  // [buffer][tile][k]
+    auto load = [&](int64_t k, float (&xo)[2][4], float (&wo)[2][4]) {
+      const int64_t kk = k + 4 * g;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t m = m0 + 16 * i + c, n = n0 + 16 * i + c;
+        if (m < a.T && kk + 4 <= k1) {
+          const f32x4u v = *reinterpret_cast<const f32x4u*>(X + m * a.K + kk);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) xo[i][q] = v[q];
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) xo[i][q] = m < a.T && kk + q < k1 ? X[m * a.K + kk + q] : 0.0f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) wo[i][q] = n < a.N && kk + q < k1 ? W[(kk + q) * a.N + n] : 0.0f;
+      }
+    };
+    auto mma = [&](const float (&xi)[2][4], const float (&wi)[2][4]) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xi[i][q], wi[j][q], acc[i][j], 0, 0, 0);
+    };
+    if (k0 < k1) load(k0, x[0], wv[0]);
+    for (int64_t k = k0; k < k1; k += 32) {
+      if (k + 16 < k1) load(k + 16, x[1], wv[1]);
+      mma(x[0], wv[0]);
+      if (k + 32 < k1) load(k + 32, x[0], wv[0]);
+      if (k + 16 < k1) mma(x[1], wv[1]);
+    }
+  }
+  if constexpr (KSPLIT) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) red[w][2 * i + j][lane] = acc[i][j];
+  }
+  __syncthreads();
+  // tile (i, j) of the wavefront: rows m0 + 16 i + 4 g + v, column n0 + 16 j + c
+  auto finish = [&](int i, int j, f32x4 y) {
+    const int64_t n = n0 + 16 * j + c;
+    if (n >= a.N) return;
+    const int row = (int)(m0 - mt) + 16 * i + 4 * g;
+    int id[4];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      id[v] = ids[row + v];
+      if (a.W == nullptr && mt + row + v < a.T) y[v] = static_cast<const float*>(a.Y)[(mt + row + v) * a.N + n];
+    }
+    const float* B = static_cast<const float*>(a.B);
+    const int64_t bs = (int64_t)a.r * a.N;
+    if (id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
+      if (id[0] >= 0)
+#pragma unroll 4
+        for (int k = 0; k < a.r; ++k) {
+          const float b = B[id[0] * bs + (int64_t)k * a.N + n];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) y[v] = fmaf(us[row + v][k], b, y[v]);
+        }
+    } else {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        if (id[v] >= 0)
+#pragma unroll 4
+          for (int k = 0; k < a.r; ++k) y[v] = fmaf(us[row + v][k], B[id[v] * bs + (int64_t)k * a.N + n], y[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      if (mt + row + v < a.T) static_cast<float*>(a.Y)[(mt + row + v) * a.N + n] = y[v];
+  };
+  if constexpr (KSPLIT) {
+    finish(w >> 1, w & 1, ((red[0][w][lane] + red[1][w][lane]) + red[2][w][lane]) + red[3][w][lane]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) finish(i, j, acc[i][j]);
   }
 }
 
@@ -826,40 +937,22 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
       return LORA_OK;
     }
     TraceScope ts("multi_expand", st);
-    hipLaunchKernelGGL(multi_expand_kernel<uint16_t>, dim3((unsigned)(cdiv(d->N, 512) * cdiv(d->T, 4))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(multi_expand_kernel, dim3((unsigned)(cdiv(d->N, 512) * cdiv(d->T, 4))), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
     return LORA_OK;
   }
-  if (W) {
-    GemmArgs g{};
-    g.M = d->T;
-    g.nseg = 1;
-    g.nreg = 1;
-    g.epi = EPI_STORE;
-    g.bkind = B_NN;
-    g.seg[0].A = X;
-    g.seg[0].lda = d->K;
-    g.seg[0].K = d->K;
-    g.seg[0].b[0][0].p = W;
-    g.seg[0].b[0][0].ld = d->N;
-    g.reg[0].N = d->N;
-    g.reg[0].out = Y;
-    g.reg[0].ldo = d->N;
-    g.ksplit = 1;
-    g.ntile_m = cdiv(d->T, gemm_tile_rows(false));
-    g.ntile_n = cdiv(d->N, gemm_tile_cols(false, false));
-    LAUNCHN("gemm_nn_store_f32", st, launch_gemm_f32(g, st));
-  }
   if (d->n > 0) {
-    {
-      TraceScope ts("multi_shrink_f32", st);
-      hipLaunchKernelGGL(multi_shrink_f32_kernel, dim3((unsigned)d->T), dim3(256), 0, st, a);
-      LAUNCH(hipGetLastError());
-    }
-    TraceScope ts("multi_expand_f32", st);
-    hipLaunchKernelGGL(multi_expand_kernel<float>, dim3((unsigned)(cdiv(d->N, 64) * cdiv(d->T, 4))), dim3(256), 0, st, a);
+    TraceScope ts("multi_shrink_f32", st);
+    hipLaunchKernelGGL(multi_shrink_f32_kernel, dim3((unsigned)d->T), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
+  } else if (W == nullptr) {
+    return LORA_OK;
   }
+  TraceScope ts("multi_f32", st);
+  const int64_t big = cdiv(d->T, 64) * cdiv(d->N, 64), small = cdiv(d->T, 32) * cdiv(d->N, 32);
+  if (big >= 512) hipLaunchKernelGGL(multi_f32_kernel<false>, dim3((unsigned)big), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(multi_f32_kernel<true>, dim3((unsigned)small), dim3(256), 0, st, a);
+  LAUNCH(hipGetLastError());
   return LORA_OK;
 }
 
