@@ -36,8 +36,10 @@ namespace {
 
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kChunk = 512;     // long-side elements per block of the passes over U
 constexpr int kMaxGroups = 24;  // stacks per launch (their table is a kernel argument)
+constexpr int kSub = 2048;      // elements of U that a wavefront takes at a time, at most
+constexpr int kVecs = kSub / 256;    // 4-element vectors per lane of them
+constexpr int kRegion = 2560 + 64;   // floats of LDS a wavefront holds them in
 
 // One stack of `count` matrices with the same shape.
 struct OrthGroup {
@@ -49,6 +51,11 @@ struct OrthGroup {
   int32_t n, r; // long and short side
   int32_t wide; // 1: [r, n], 0: [n, r]
   int32_t count, chunks;
+  int32_t sub, pitch;  // long-side elements per sub-tile (wide: a power of two), and its row pitch in LDS
+  int32_t sub_log2;
+  uint32_t inv_r;      // ceil(2^20 / r): e inv_r >> 20 = e / r for e < 2^11 + 2^9
+  int32_t vec_lds;     // vectors of four stay within a row of LDS
+  int32_t nsub;        // sub-tiles per wavefront and block
   int32_t blk0; // first block of the group in the passes over U
   int32_t mat0; // first block of the group in the r x r steps
   float scale;
@@ -63,126 +70,135 @@ struct OrthArgs {
   double decay, lr;  // P <- decay P - lr scale O
 };
 
-// Up to four consecutive elements with no more alignment than their own.
-template <typename T, int N>
-struct Run;
-template <int N>
-struct Run<float, N> {
-  typedef float vec __attribute__((ext_vector_type(N), aligned(4)));
-  static __device__ __forceinline__ void load(const float* p, float (&x)[N]) {
-    const vec v = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = v[i];
-  }
-  static __device__ __forceinline__ void store(float* p, const float (&x)[N]) {
-    vec v;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = x[i];
-    *reinterpret_cast<vec*>(p) = v;
-  }
-};
-template <>
-struct Run<float, 1> {
-  static __device__ __forceinline__ void load(const float* p, float (&x)[1]) { x[0] = *p; }
-  static __device__ __forceinline__ void store(float* p, const float (&x)[1]) { *p = x[0]; }
-};
-template <int N>
-struct Run<uint16_t, N> {
-  typedef uint16_t vec __attribute__((ext_vector_type(N), aligned(2)));
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&x)[N]) {
-    const vec v = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = bf2f(v[i]);
-  }
-  static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[N]) {
-    vec v;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = (uint16_t)f2bf(x[i]);
-    *reinterpret_cast<vec*>(p) = v;
-  }
-};
-template <>
-struct Run<uint16_t, 1> {
-  static __device__ __forceinline__ void load(const uint16_t* p, float (&x)[1]) { x[0] = bf2f(*p); }
-  static __device__ __forceinline__ void store(uint16_t* p, const float (&x)[1]) { *p = (uint16_t)f2bf(x[0]); }
-};
+// Four consecutive elements with no more alignment than their own.
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
+  return *reinterpret_cast<const v4*>(p);
+}
+__device__ __forceinline__ f32x4 load4(const uint16_t* p) {
+  typedef uint16_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+  const v4 v = *reinterpret_cast<const v4*>(p);
+  return f32x4{bf2f(v[0]), bf2f(v[1]), bf2f(v[2]), bf2f(v[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4 x) {
+  typedef float v4 __attribute__((ext_vector_type(4), aligned(4)));
+  *reinterpret_cast<v4*>(p) = x;
+}
+__device__ __forceinline__ void store4(uint16_t* p, f32x4 x) {
+  typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
+  *reinterpret_cast<v2*>(p) = v2{pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3])};
+}
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf2f(*p); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = (uint16_t)f2bf(x); }
 
-// A vector type of three would be read and written as four.
+// The first `valid` of four elements (the rest read 0).
 template <typename T>
-struct Run3 {
-  static __device__ __forceinline__ void load(const T* p, float (&x)[3]) {
-    float a[2], b[1];
-    Run<T, 2>::load(p, a);
-    Run<T, 1>::load(p + 2, b);
-    x[0] = a[0];
-    x[1] = a[1];
-    x[2] = b[0];
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&x)[3]) {
-    const float a[2] = {x[0], x[1]}, b[1] = {x[2]};
-    Run<T, 2>::store(p, a);
-    Run<T, 1>::store(p + 2, b);
-  }
-};
-
-template <>
-struct Run<float, 3> : Run3<float> {};
-template <>
-struct Run<uint16_t, 3> : Run3<uint16_t> {};
-
-// N consecutive elements of which the first `valid` exist (the rest read 0).
-template <typename T, int N>
-__device__ __forceinline__ void load_run(const T* p, int valid, float (&x)[N]) {
-  if constexpr (N > 4) {
+__device__ __forceinline__ f32x4 load_some(const T* p, int valid) {
+  if (valid >= 4) return load4(p);
+  f32x4 x = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < N; j += 4) {
-      float y[4];
-      load_run<T, 4>(p + j, valid - j, y);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[j + i] = y[i];
-    }
-  } else if (valid >= N) {
-    Run<T, N>::load(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float y[1] = {0.0f};
-      if (i < valid) Run<T, 1>::load(p + i, y);
-      x[i] = y[0];
-    }
-  }
+  for (int i = 0; i < 3; ++i)
+    if (i < valid) x[i] = load1(p + i);
+  return x;
 }
-template <typename T, int N>
-__device__ __forceinline__ void store_run(T* p, int valid, const float (&x)[N]) {
-  if (valid >= N) {
-    Run<T, N>::store(p, x);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float y[1] = {x[i]};
-      if (i < valid) Run<T, 1>::store(p + i, y);
-    }
-  }
-}
-
-// U at elements o .. o + N - 1 of a stack.  FIRST: the momentum is brought up
-// to date (M <- mu M + G) and stored; later passes read the new one.
-template <typename T, int N, bool FIRST>
-__device__ __forceinline__ void load_u(const OrthArgs& a, const OrthGroup& g, int64_t o, int valid, float (&u)[N]) {
-  const T* G = static_cast<const T*>(g.G);
-  if (!a.muon) {
-    load_run<T, N>(G + o, valid, u);
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int valid, f32x4 x) {
+  if (valid >= 4) {
+    store4(p, x);
     return;
   }
-  float m[N], x[N];
-  load_run<float, N>(g.M + o, valid, m);
-  if (FIRST || a.nesterov) load_run<T, N>(G + o, valid, x);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (FIRST) m[i] = fmaf(a.mu, m[i], x[i]);
-    u[i] = a.nesterov ? fmaf(a.mu, m[i], x[i]) : m[i];
+  for (int i = 0; i < 3; ++i)
+    if (i < valid) store1(p + i, x[i]);
+}
+
+// Hand-off between the lanes of a wavefront through its own LDS region.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// A sub-tile of one matrix: `len` (at most g.sub) long-side elements from l0.
+// Its elements are numbered as they lie in memory, tall: row by row, wide: row
+// by row of g.sub columns, and vector j of a lane holds four of them from
+// 4 (64 j + lane), so every global access is 16 (or, in bf16, 8) bytes of a
+// contiguous run whatever the rank.  In LDS element (row, column) is at
+// row * pitch + column.
+struct SubTile {
+  int64_t base;  // of the sub-tile in its tensor
+  int len, total;
+  // vector j: its global offset and how many of its elements exist
+  __device__ __forceinline__ int64_t at(const OrthGroup& g, int j, int& valid, int& row, int& col) const {
+    const int e = 4 * (64 * j + (threadIdx.x & 63));
+    if (!g.wide) {
+      row = (int)(((uint32_t)e * g.inv_r) >> 20);
+      col = e - row * g.r;
+      valid = len * g.r - e;
+      return base + e;
+    }
+    row = e >> g.sub_log2;
+    col = e & (g.sub - 1);
+    valid = row < g.r ? len - col : 0;
+    return base + (int64_t)row * g.n + col;
   }
-  if (FIRST) store_run<float, N>(g.M + o, valid, m);
+};
+// The four elements of a vector that starts at (row, column): a tall one may run over row ends.
+template <typename F>
+__device__ __forceinline__ void each4(const OrthGroup& g, int row, int col, F&& f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f(i, row * g.pitch + col);
+    if (++col == g.r && !g.wide) {
+      col = 0;
+      ++row;
+    }
+  }
+}
+__device__ __forceinline__ void put4(const OrthGroup& g, float* lds, int row, int col, f32x4 x) {
+  if (g.vec_lds) *reinterpret_cast<f32x4*>(lds + row * g.pitch + col) = x;
+  else each4(g, row, col, [&](int i, int o) { lds[o] = x[i]; });
+}
+__device__ __forceinline__ f32x4 get4(const OrthGroup& g, const float* lds, int row, int col) {
+  if (g.vec_lds) return *reinterpret_cast<const f32x4*>(lds + row * g.pitch + col);
+  f32x4 x;
+  each4(g, row, col, [&](int i, int o) { x[i] = lds[o]; });
+  return x;
+}
+
+// U of a sub-tile into LDS (zeros past len).  FIRST: the momentum is brought
+// up to date (M <- mu M + G) and stored; later passes read the new one.  All
+// of a lane's loads are issued before the first is waited for.
+template <typename T, bool FIRST>
+__device__ __forceinline__ void load_u(const OrthArgs& a, const OrthGroup& g, const SubTile& st, float* lds) {
+  const T* G = static_cast<const T*>(g.G);
+  const bool need_g = !a.muon || FIRST || a.nesterov;
+  f32x4 x[kVecs], m[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    int valid, row, col;
+    const int64_t o = st.at(g, j, valid, row, col);
+    x[j] = m[j] = f32x4{0, 0, 0, 0};
+    if (need_g) x[j] = load_some(G + o, valid);
+    if (a.muon) m[j] = load_some(g.M + o, valid);
+  }
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    int valid, row, col;
+    const int64_t o = st.at(g, j, valid, row, col);
+    f32x4 u = x[j];
+    if (a.muon) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (FIRST) m[j][i] = fmaf(a.mu, m[j][i], x[j][i]);
+        u[i] = a.nesterov ? fmaf(a.mu, m[j][i], x[j][i]) : m[j][i];
+      }
+      if (FIRST) store_some(g.M + o, valid, m[j]);
+    }
+    if (4 * (64 * j + (int)(threadIdx.x & 63)) < st.total) put4(g, lds, row, col, u);
+  }
 }
 
 // The group of block b (first blocks blk0 or mat0 ascending).
@@ -193,254 +209,313 @@ __device__ __forceinline__ int find_group(const OrthArgs& a, int b, bool mats) {
   return __builtin_amdgcn_readfirstlane(k);
 }
 
-// Partial U^T U of one matrix over kChunk of its long side: four wavefronts
-// share the chunk.  An operand of tile t holds, in lane 16 q + c, U at long
-// index k + q (any assignment of the four k to the lane groups gives the same
-// sum) and short index NT c + t, and serves as both sides of the product.
-// Only the tiles on and above the diagonal are formed.
+// Where a wavefront of block b works: its group, matrix and chunk, and the
+// sub-tiles of the chunk that are its own.
+struct Place {
+  int mat, chunk;
+  __device__ __forceinline__ Place(const OrthGroup& g, int b) : mat(b / g.chunks), chunk(b % g.chunks) {}
+  __device__ __forceinline__ SubTile sub(const OrthGroup& g, int w, int i) const {
+    const int l0 = ((chunk * 4 + w) * g.nsub + i) * g.sub;
+    SubTile st;
+    st.len = g.n - l0 < g.sub ? g.n - l0 : g.sub;
+    st.total = g.sub * g.r;
+    st.base = (int64_t)mat * g.n * g.r + (g.wide ? (int64_t)l0 : (int64_t)l0 * g.r);
+    return st;
+  }
+};
+
+// Partial U^T U of one matrix over one chunk of its long side.  An operand of
+// tile t holds, in lane 16 q + c, U at long index k + q (any assignment of the
+// four k to the lane groups gives the same sum) and short index NT c + t, and
+// serves as both sides of the product.  Only the tiles on and above the
+// diagonal are formed.  The wavefronts work alone until their sums meet.
 template <typename T, int NT>
 __global__ __launch_bounds__(256) void orth_gram_kernel(const OrthArgs a) {
   constexpr int NP = NT * (NT + 1) / 2;
-  __shared__ double red[3][NP * 4 * 64];
+  __shared__ __attribute__((aligned(16))) float us[4][kRegion];
+  constexpr int AT = NT == 4 ? 5 : NP;  // tiles whose sums meet at a time, in the regions
+  static_assert(sizeof(double) * 3 * AT * 256 <= sizeof(us) && NP % AT == 0, "the exchange fits the regions");
+  double* const red = reinterpret_cast<double*>(&us[0][0]);
   const OrthGroup& g = a.g[find_group(a, blockIdx.x, false)];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
-  const int b = (int)blockIdx.x - g.blk0, mat = b / g.chunks, chunk = b % g.chunks;
-  const int64_t base = (int64_t)mat * g.n * g.r;
-  const int k0 = chunk * kChunk + w * (kChunk / 4);
-  const int left = g.n - k0;
-  const int len = left < kChunk / 4 ? left : kChunk / 4;
+  const Place at(g, (int)blockIdx.x - g.blk0);
+  float* const u = us[w];
   f64x4 acc[NP];
 #pragma unroll
   for (int i = 0; i < NP; ++i) acc[i] = f64x4{0, 0, 0, 0};
-  auto mma = [&](const float (&u)[NT]) {
+  auto mma = [&](const float (&x)[NT]) {
     double d[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) d[t] = (double)u[t];
+    for (int t = 0; t < NT; ++t) d[t] = (double)x[t];
     int i = 0;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int s = t; s < NT; ++s, ++i) acc[i] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[t], d[s], acc[i], 0, 0, 0);
   };
-  if (!g.wide) {
-    constexpr int UN = NT == 1 ? 8 : 4;
-    const int valid = g.r - NT * c;
-    for (int k = 0; k < len; k += 4 * UN) {
-      float u[UN][NT];
+  for (int i = 0; i < g.nsub; ++i) {
+    const SubTile st = at.sub(g, w, i);
+    if (st.len <= 0) break;
+    load_u<T, true>(a, g, st, u);
+    wave_sync();
+    if (!g.wide) {
+#pragma unroll 4
+      for (int k = 0; k < st.len; k += 4) {  // rows up to the sub-tile's (a multiple of 16) are zero past len
+        float x[NT];
 #pragma unroll
-      for (int j = 0; j < UN; ++j) {
-        const int kk = k + 4 * j + q;
-        load_u<T, NT, true>(a, g, base + (int64_t)(k0 + kk) * g.r + NT * c, kk < len ? valid : 0, u[j]);
+        for (int t = 0; t < NT; ++t) x[t] = NT * c + t < g.r ? u[(k + q) * g.pitch + NT * c + t] : 0.0f;
+        mma(x);
       }
+    } else {
+      for (int k = 0; k < st.len; k += 16) {
+        f32x4 y[NT];
 #pragma unroll
-      for (int j = 0; j < UN; ++j) mma(u[j]);
-    }
-  } else {
-    constexpr int UN = NT == 1 ? 4 : NT == 2 ? 2 : 1;
-    for (int k = 0; k < len; k += 16 * UN) {
-      float u[UN][NT][4];
-#pragma unroll
-      for (int j = 0; j < UN; ++j)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const int kk = k + 16 * j + 4 * q, i = NT * c + t;
-          load_u<T, 4, true>(a, g, base + (int64_t)i * g.n + k0 + kk, i < g.r ? len - kk : 0, u[j][t]);
-        }
-#pragma unroll
-      for (int j = 0; j < UN; ++j)
+        for (int t = 0; t < NT; ++t)
+          y[t] = NT * c + t < g.r ? *reinterpret_cast<const f32x4*>(u + (NT * c + t) * g.pitch + k + 4 * q) : f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           float x[NT];
 #pragma unroll
-          for (int t = 0; t < NT; ++t) x[t] = u[j][t][v];
+          for (int t = 0; t < NT; ++t) x[t] = y[t][v];
           mma(x);
         }
-    }
-  }
-  if (w > 0)
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[w - 1][(i * 4 + v) * 64 + lane] = acc[i][v];
-  __syncthreads();
-  if (w == 0) {
-    double* out = g.part + ((int64_t)mat * g.chunks + chunk) * (NP * 256);
-#pragma unroll
-    for (int i = 0; i < NP; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int o = (i * 4 + v) * 64 + lane;
-        out[o] = acc[i][v] + red[0][o] + red[1][o] + red[2][o];
       }
+    }
+    wave_sync();
+  }
+  double* out = g.part + ((int64_t)at.mat * g.chunks + at.chunk) * (NP * 256);
+#pragma unroll
+  for (int i0 = 0; i0 < NP; i0 += AT) {
+    __syncthreads();
+    if (w > 0)
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) red[((w - 1) * AT * 4 + i * 4 + v) * 64 + lane] = acc[i0 + i][v];
+    __syncthreads();
+    if (w == 0)
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int o = (i * 4 + v) * 64 + lane;
+          out[i0 * 256 + o] = acc[i0 + i][v] + red[o] + red[AT * 256 + o] + red[2 * AT * 256 + o];
+        }
   }
 }
 
-// The steps of one matrix on its r x r Gram matrix, one block of four
-// wavefronts.  Per step: p = a I + b G + c G G; V = G p and Q <- Q p; G <- V p.
-// All matrices are symmetric, so both operands of a product are read along
-// rows; rows are 16 NT + 2 doubles apart, which spreads the 16 rows of a
-// fragment read over all banks.
+// The steps of one matrix on its r x r Gram matrix, one block.  Per step:
+// p = a I + b G + c G G; V = G p and Q <- Q p; G <- V p.  All matrices are
+// symmetric and commute, so both operands of a product are read along rows,
+// and only the tiles on and above the diagonal are formed (10 of 16 at NT =
+// 4) and written to both sides.  A matrix has only its CU's matrix cores, 2048
+// flops in 64 cycles each, and at NT = 4 that is the bound: one tile a
+// wavefront, so that the four matrix cores share each product evenly and one
+// wavefront's LDS reads hide behind another's MFMAs.  Rows are 16 NT + 2
+// doubles apart, which spreads the 16 rows of a fragment read over all banks.
 template <int NT>
-__global__ __launch_bounds__(256) void orth_steps_kernel(const OrthArgs a) {
-  constexpr int N = 16 * NT, LD = N + 2, NP = NT * (NT + 1) / 2, TILES = NT * NT, PER = (TILES + 3) / 4;
+__global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(const OrthArgs a) {
+  constexpr int N = 16 * NT, LD = N + 2, NP = NT * (NT + 1) / 2, THREADS = NT >= 3 ? 1024 : 256 * NT;
+  constexpr int WAVES = THREADS / 64;
   __shared__ double mg[N * LD], mp[N * LD], mv[N * LD], mq[N * LD];
   const OrthGroup& g = a.g[find_group(a, blockIdx.x, true)];
   const int mat = (int)blockIdx.x - g.mat0;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
 
   // sum of the chunks, ascending; element (i, v, lane) is row 16 t + 4 v + q, column 16 s + c
   const double* part = g.part + (int64_t)mat * g.chunks * (NP * 256);
-  for (int e = threadIdx.x; e < NP * 256; e += 256) {
+  for (int e = threadIdx.x; e < NP * 256; e += THREADS) {
     double s = 0.0;
-#pragma unroll 8
+#pragma unroll 16
     for (int k = 0; k < g.chunks; ++k) s += part[(int64_t)k * (NP * 256) + e];
     const int i = e >> 8, v = (e >> 6) & 3, l = e & 63;
     int t = 0, first = 0;
     while (i >= first + NT - t) first += NT - t++;
     const int row = 16 * t + 4 * v + (l >> 4), col = 16 * (t + i - first) + (l & 15);
     mg[row * LD + col] = s;
-    if (t != t + i - first) mg[col * LD + row] = s;
+    if (i != first) mg[col * LD + row] = s;
   }
   __syncthreads();
-  double trace = 0.0;
-  for (int i = 0; i < N; ++i) trace += mg[i * LD + i];
+  double trace = lane < N ? mg[lane * LD + lane] : 0.0;
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
   const double inv = 1.0 / (sqrt(trace) + a.eps);
   __syncthreads();
-  for (int e = threadIdx.x; e < N * N; e += 256) {
-    const int row = e / N, col = e % N;
-    mg[row * LD + col] *= inv * inv;
-    mq[row * LD + col] = row == col ? 1.0 : 0.0;
-  }
+  for (int e = threadIdx.x; e < N * N; e += THREADS) mg[e / N * LD + e % N] *= inv * inv;
   __syncthreads();
-
-  f64x4 x[PER], y[PER];
-  // this wavefront's tiles of the product A B
-  auto product = [&](const double* A, const double* B, f64x4 (&o)[PER]) {
+  auto product = [&](const double* A, const double* B, int t, int s) {
+    f64x4 o = f64x4{0, 0, 0, 0};
+    const double* ar = A + (16 * t + c) * LD + q;
+    const double* br = B + (16 * s + c) * LD + q;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      o[j] = f64x4{0, 0, 0, 0};
-      const int tile = w + 4 * j;
-      if (tile < TILES) {
-        const double* ar = A + (16 * (tile / NT) + c) * LD + q;
-        const double* br = B + (16 * (tile % NT) + c) * LD + q;
+    for (int k = 0; k < N / 4; ++k) o = __builtin_amdgcn_mfma_f64_16x16x4f64(ar[4 * k], br[4 * k], o, 0, 0, 0);
+    return o;
+  };
+  auto corner = [&](int i, int& t, int& s) {  // tile i of the upper triangle, row by row
+    int first = 0;
+    t = 0;
+    while (i >= first + NT - t) first += NT - t++;
+    s = t + i - first;
+  };
+  auto put = [&](double* D, int t, int s, int v, double x) {
+    const int row = 16 * t + 4 * v + q, col = 16 * s + c;
+    D[row * LD + col] = x;
+    if (t != s) D[col * LD + row] = x;
+  };
+  constexpr int MOST = (2 * NP + WAVES - 1) / WAVES;  // tiles of a pair of products per wavefront
+  f64x4 x[MOST];
+  for (int k = 0; k < a.steps; ++k) {
+    const bool last = k + 1 == a.steps;
+    for (int i = w; i < NP; i += WAVES) {
+      int t, s;
+      corner(i, t, s);
+      const f64x4 o = product(mg, mg, t, s);
 #pragma unroll
-        for (int s = 0; s < N / 4; ++s) o[j] = __builtin_amdgcn_mfma_f64_16x16x4f64(ar[4 * s], br[4 * s], o[j], 0, 0, 0);
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * t + 4 * v + q, col = 16 * s + c;
+        const double p = fma(a.c, o[v], a.b * mg[row * LD + col]) + (row == col ? a.a : 0.0);
+        put(mp, t, s, v, p);
+        if (k == 0) put(mq, t, s, v, p);  // Q = I before
       }
     }
-  };
-  // f(row, column, element) over this wavefront's tiles
-  auto each = [&](f64x4 (&o)[PER], auto f) {
+    __syncthreads();
+    // product 0: V = G p (unless this is the last step), product 1: Q p (unless it is the first)
+    const bool need[2] = {!last, k > 0};
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int tile = w + 4 * j;
-      if (tile < TILES)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) f(16 * (tile / NT) + 4 * v + q, 16 * (tile % NT) + c, o[j][v]);
+    for (int j = 0; j < MOST; ++j) {
+      const int i = w + j * WAVES;
+      if (i < 2 * NP && need[i >= NP]) {
+        int t, s;
+        corner(i >= NP ? i - NP : i, t, s);
+        x[j] = product(i >= NP ? mq : mg, mp, t, s);
+      }
     }
-  };
-  for (int k = 0; k < a.steps; ++k) {
-    product(mg, mg, x);
-    each(x, [&](int row, int col, double s) {
-      mp[row * LD + col] = fma(a.c, s, a.b * mg[row * LD + col]) + (row == col ? a.a : 0.0);
-    });
     __syncthreads();
-    const bool last = k + 1 == a.steps;
-    product(mq, mp, x);
-    if (!last) product(mg, mp, y);
+#pragma unroll
+    for (int j = 0; j < MOST; ++j) {
+      const int i = w + j * WAVES;
+      if (i < 2 * NP && need[i >= NP]) {
+        int t, s;
+        corner(i >= NP ? i - NP : i, t, s);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) put(i >= NP ? mq : mv, t, s, v, x[j][v]);
+      }
+    }
     __syncthreads();
-    each(x, [&](int row, int col, double s) { mq[row * LD + col] = s; });
     if (last) break;
-    each(y, [&](int row, int col, double s) { mv[row * LD + col] = s; });
-    __syncthreads();
-    product(mv, mp, x);
-    each(x, [&](int row, int col, double s) { mg[row * LD + col] = s; });
+    for (int i = w; i < NP; i += WAVES) {
+      int t, s;
+      corner(i, t, s);
+      const f64x4 o = product(mv, mp, t, s);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) put(mg, t, s, v, o[v]);
+    }
     __syncthreads();
   }
-  __syncthreads();
   double* Q = g.Q + (int64_t)mat * N * N;
-  for (int e = threadIdx.x; e < N * N; e += 256) Q[e] = mq[e / N * LD + e % N] * inv;
+  for (int e = threadIdx.x; e < N * N; e += THREADS) Q[e] = mq[e / N * LD + e % N] * inv;
 }
 
-// O = U Q (tall) or Q U (wide) over kChunk of the long side, and its use.
+// O = U Q (tall) or Q U (wide) over one chunk of the long side, and its use.
+// A wavefront works alone on each of its sub-tiles: U goes to LDS, 16 rows
+// (columns) at a time are multiplied and replaced there by O, which is then
+// read back as it lies in memory for the update of P (loaded with U).
 template <typename T, int NT>
 __global__ __launch_bounds__(256) void orth_apply_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, S = N / 4;
+  __shared__ __attribute__((aligned(16))) float us[4][kRegion];
   __shared__ double mq[N * LD];
   const OrthGroup& g = a.g[find_group(a, blockIdx.x, false)];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
-  const int b = (int)blockIdx.x - g.blk0, mat = b / g.chunks, chunk = b % g.chunks;
-  const double* Q = g.Q + (int64_t)mat * N * N;
+  const Place at(g, (int)blockIdx.x - g.blk0);
+  const double* Q = g.Q + (int64_t)at.mat * N * N;
   for (int e = threadIdx.x; e < N * N; e += 256) mq[e / N * LD + e % N] = Q[e];
-  __syncthreads();
-  const int64_t base = (int64_t)mat * g.n * g.r;
   T* const P = static_cast<T*>(g.P);
   const double lrs = a.lr * (double)g.scale;
-  auto use = [&](double o, float p) { return a.muon ? (float)fma(a.decay, (double)p, -lrs * o) : (float)o; };
-  const int k1 = chunk * kChunk + kChunk < g.n ? chunk * kChunk + kChunk : g.n;
-  if (!g.wide) {
-    // 16 rows a time: lane 16 q + c holds row c, short indices S q .. S q + S - 1, and ends with
-    // rows 4 v + q, short indices NT c .. NT c + NT - 1
-    for (int k = chunk * kChunk + 16 * w; k < k1; k += 64) {
-      float u[S];
-      load_u<T, S, false>(a, g, base + (int64_t)(k + c) * g.r + S * q, k + c < k1 ? g.r - S * q : 0, u);
-      f64x4 acc[NT];
+  float* const u = us[w];
+  __syncthreads();
+  for (int i = 0; i < g.nsub; ++i) {
+    const SubTile st = at.sub(g, w, i);
+    if (st.len <= 0) break;
+    f32x4 p[kVecs];
+    if (a.muon)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = f64x4{0, 0, 0, 0};
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const int i = S * q + s, label = 16 * (i % NT) + i / NT;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)u[s], mq[label * LD + 16 * t + c], acc[t], 0, 0, 0);
+      for (int j = 0; j < kVecs; ++j) {
+        int valid, row, col;
+        const int64_t o = st.at(g, j, valid, row, col);
+        p[j] = load_some(P + o, valid);
       }
+    load_u<T, false>(a, g, st, u);
+    wave_sync();
+    if (!g.wide) {
+      // lane 16 q + c reads row c, short indices S q .. S q + S - 1, and ends with rows 4 v + q,
+      // short indices NT c .. NT c + NT - 1
+      for (int k = 0; k < st.len; k += 16) {
+        float x[S];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int row = k + 4 * v + q, valid = row < k1 ? g.r - NT * c : 0;
-        const int64_t o = base + (int64_t)row * g.r + NT * c;
-        float p[NT];
-        if (a.muon) load_run<T, NT>(P + o, valid, p);
+        for (int s = 0; s < S; ++s) x[s] = S * q + s < g.r ? u[(k + c) * g.pitch + S * q + s] : 0.0f;
+        f64x4 acc[NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) p[t] = use(acc[t][v], p[t]);
-        store_run<T, NT>(P + o, valid, p);
-      }
-    }
-  } else {
-    // 64 columns a time: lane 16 q + c holds columns 4 c .. 4 c + 3 of the rows with labels
-    // 4 s + q, and ends with the same columns of the rows with labels 16 t + 4 v + q
-    for (int k = chunk * kChunk + 64 * w; k < k1; k += 256) {
-      const int col = k + 4 * c, valid = k1 - col;
-      float u[S][4];
-#pragma unroll
-      for (int s = 0; s < S; ++s) {
-        const int label = 4 * s + q, i = NT * (label % 16) + label / 16;
-        load_u<T, 4, false>(a, g, base + (int64_t)i * g.n + col, i < g.r ? valid : 0, u[s]);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f64x4 acc[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = f64x4{0, 0, 0, 0};
+        for (int t = 0; t < NT; ++t) acc[t] = f64x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-          const double m = mq[(16 * t + c) * LD + 4 * s + q];
+          const int label = 16 * (s % NT) + 4 * q + s / NT;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j] = __builtin_amdgcn_mfma_f64_16x16x4f64(m, (double)u[s][j], acc[j], 0, 0, 0);
+          for (int t = 0; t < NT; ++t)
+            acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[s], mq[label * LD + 16 * t + c], acc[t], 0, 0, 0);
         }
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int i = NT * (4 * v + q) + t;
-          const int64_t o = base + (int64_t)i * g.n + col;
-          float p[4];
-          if (a.muon) load_run<T, 4>(P + o, i < g.r ? valid : 0, p);
+        for (int v = 0; v < 4; ++v)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = use(acc[j][v], p[j]);
-          store_run<T, 4>(P + o, i < g.r ? valid : 0, p);
+          for (int t = 0; t < NT; ++t)
+            if (NT * c + t < g.r) u[(k + 4 * v + q) * g.pitch + NT * c + t] = (float)acc[t][v];
+      }
+    } else {
+      // lane 16 q + c reads column c of the rows with labels 4 s + q, and ends with that column of
+      // the rows with labels 16 t + 4 v + q
+      for (int k = 0; k < st.len; k += 16) {
+        float x[S];
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          const int row = NT * (4 * (s % 4) + q) + s / 4;
+          x[s] = row < g.r ? u[row * g.pitch + k + c] : 0.0f;
         }
+        f64x4 acc[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[t] = f64x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64(mq[(16 * t + c) * LD + 4 * s + q], (double)x[s], acc[t], 0, 0, 0);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int row = NT * (4 * v + q) + t;
+            if (row < g.r) u[row * g.pitch + k + c] = (float)acc[t][v];
+          }
       }
     }
+    wave_sync();
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      int valid, row, col;
+      const int64_t o = st.at(g, j, valid, row, col);
+      if (valid <= 0) continue;
+      f32x4 x = get4(g, u, row, col);
+      if (a.muon)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x[v] = (float)fma(a.decay, (double)p[j][v], -lrs * (double)x[v]);
+      store_some(P + o, valid, x);
+    }
+    wave_sync();
   }
 }
 
@@ -454,7 +529,7 @@ hipError_t launch_orth(const OrthArgs& a, int blocks, int mats, hipStream_t st) 
   }
   {
     TraceScope ts("orth_steps", st);
-    hipLaunchKernelGGL((orth_steps_kernel<NT>), dim3((unsigned)mats), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((orth_steps_kernel<NT>), dim3((unsigned)mats), dim3(NT >= 3 ? 1024 : 256 * NT), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -477,14 +552,30 @@ hipError_t launch_orth_nt(int nt, const OrthArgs& a, int blocks, int mats, hipSt
 // ---------------------------------------------------------------------------
 struct Shape {
   int64_t n, r, chunks, nt;
+  int32_t sub, sub_log2, pitch, nsub;
   size_t part, q;  // workspace bytes
 };
 Shape shape_of(const lora_orth_mat& m) {
   Shape s;
   s.n = m.rows > m.cols ? m.rows : m.cols;
   s.r = m.rows > m.cols ? m.cols : m.rows;
-  s.chunks = cdiv(s.n, kChunk);
   s.nt = cdiv(s.r, 16);
+  // as much of the long side as kSub elements hold: a multiple of 16 rows of a tall matrix, a
+  // power of two (16 at least) of columns of a wide one.  LDS rows are padded against bank
+  // conflicts, to 16 bytes where vectors of four do not run over row ends.
+  s.sub_log2 = 0;
+  if (m.cols > m.rows) {
+    s.sub_log2 = 4;
+    while (s.sub_log2 < 8 && (2 << s.sub_log2) * s.r <= kSub) ++s.sub_log2;
+    s.sub = 1 << s.sub_log2;
+    s.pitch = s.sub + 4;
+  } else {
+    s.pitch = (int32_t)(s.r % 4 == 0 ? s.r + 4 : s.r | 1);
+    s.sub = (int32_t)std::min<int64_t>(256, std::min(kSub / s.r, 2560 / (int64_t)s.pitch) / 16 * 16);
+  }
+  // more sub-tiles per block where a partial Gram matrix is larger
+  s.nsub = (int32_t)s.nt;
+  s.chunks = cdiv(s.n, (int64_t)4 * s.sub * s.nsub);
   s.part = (size_t)(m.count * s.chunks * (s.nt * (s.nt + 1) / 2) * 256 * 8);
   s.q = (size_t)(m.count * s.nt * s.nt * 256 * 8);
   return s;
@@ -591,6 +682,7 @@ lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, OrthArg
       if (s.nt != nt || m.count == 0) continue;
       if (a.ngroups == kMaxGroups || blocks + m.count * s.chunks > ((int64_t)1 << 30)) LAUNCH(flush());
       OrthGroup& g = a.g[a.ngroups++];
+      g.wide = m.cols > m.rows;
       g.G = m.G;
       g.M = m.M;
       g.P = m.P;
@@ -598,9 +690,14 @@ lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, OrthArg
       g.Q = Q;
       g.n = (int32_t)s.n;
       g.r = (int32_t)s.r;
-      g.wide = m.cols > m.rows;
       g.count = (int32_t)m.count;
       g.chunks = (int32_t)s.chunks;
+      g.sub = s.sub;
+      g.sub_log2 = s.sub_log2;
+      g.pitch = s.pitch;
+      g.nsub = s.nsub;
+      g.inv_r = (uint32_t)cdiv((int64_t)1 << 20, s.r);
+      g.vec_lds = g.wide || s.r % 4 == 0;
       g.blk0 = (int32_t)blocks;
       g.mat0 = (int32_t)nmat;
       g.scale = m.scale;
