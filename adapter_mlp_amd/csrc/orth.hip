@@ -27,6 +27,7 @@
 #include <cmath>
 #include <memory>
 #include <new>
+#include <type_traits>
 
 #include "abi.hpp"
 #include "common.hpp"
@@ -50,21 +51,23 @@ struct OrthGroup {
   double* Q;    // [count][16 NT][16 NT]
   int32_t n, r; // long and short side
   int32_t wide; // 1: [r, n], 0: [n, r]
-  int32_t count, chunks;
+  int32_t chunks;      // blocks that form U^T U of one matrix
   int32_t sub, pitch;  // long-side elements per sub-tile (wide: a power of two), and its row pitch in LDS
   int32_t sub_log2;
   uint32_t inv_r;      // ceil(2^20 / r): e inv_r >> 20 = e / r for e < 2^11 + 2^9
   int32_t vec_lds;     // vectors of four stay within a row of LDS
-  int32_t nsub;        // sub-tiles per wavefront and block
-  int32_t blk0; // first block of the group in the passes over U
-  int32_t mat0; // first block of the group in the r x r steps
+  int32_t nsub;        // sub-tiles per wavefront of a block that forms U^T U
+  int32_t subs;        // blocks of one sub-tile per wavefront that form U Q
   float scale;
 };
 
+// The first blocks of the groups in the three launches (past the last group:
+// INT_MAX), side by side so that a few wide scalar loads bring them in.
+enum { GRAM, STEPS, APPLY };
 struct OrthArgs {
+  int32_t first[3][kMaxGroups];
   OrthGroup g[kMaxGroups];
-  int32_t ngroups, nesterov;
-  int32_t steps, muon;
+  int32_t ngroups, steps;
   float mu;
   double a, b, c, eps;
   double decay, lr;  // P <- decay P - lr scale O
@@ -121,28 +124,63 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// A sub-tile of one matrix: `len` (at most g.sub) long-side elements from l0.
-// Its elements are numbered as they lie in memory, tall: row by row, wide: row
-// by row of g.sub columns, and vector j of a lane holds four of them from
+// A sub-tile of one matrix: `len` (at most g.sub) long-side elements.  Its
+// elements are numbered as they lie in memory, tall: row by row, wide: row by
+// row of g.sub columns, and vector j of a lane holds four of them from
 // 4 (64 j + lane), so every global access is 16 (or, in bf16, 8) bytes of a
 // contiguous run whatever the rank.  In LDS element (row, column) is at
 // row * pitch + column.
 struct SubTile {
-  int64_t base;  // of the sub-tile in its tensor
+  int64_t first;        // first element
+  int64_t off, step;    // vector j of the lane is at off + j step
   int len, total;
-  // vector j: its global offset and how many of its elements exist
-  __device__ __forceinline__ int64_t at(const OrthGroup& g, int j, int& valid, int& row, int& col) const {
-    const int e = 4 * (64 * j + (threadIdx.x & 63));
-    if (!g.wide) {
-      row = (int)(((uint32_t)e * g.inv_r) >> 20);
-      col = e - row * g.r;
-      valid = len * g.r - e;
-      return base + e;
-    }
+  int col, row, rows;   // wide: column, and row of vector j: row + j rows
+  __device__ __forceinline__ SubTile(const OrthGroup& g, int mat, int i) {
+    const int l0 = i * g.sub, e = 4 * ((int)threadIdx.x & 63);
+    const int64_t base = (int64_t)mat * g.n * g.r;
+    len = g.n - l0 < g.sub ? g.n - l0 : g.sub;
+    total = g.sub * g.r;
     row = e >> g.sub_log2;
     col = e & (g.sub - 1);
-    valid = row < g.r ? len - col : 0;
-    return base + (int64_t)row * g.n + col;
+    rows = 256 >> g.sub_log2;  // g.sub is at most 256
+    first = base + (g.wide ? (int64_t)l0 : (int64_t)l0 * g.r);
+    off = first + (g.wide ? (int64_t)row * g.n + col : (int64_t)e);
+    step = g.wide ? (int64_t)rows * g.n : 256;
+  }
+  // how many elements of vector j exist (four at least: all)
+  __device__ __forceinline__ int valid(const OrthGroup& g, int j) const {
+    const int tall = len * g.r - 4 * (64 * j + ((int)threadIdx.x & 63)), wide = row + j * rows < g.r ? len - col : 0;
+    return g.wide ? wide : tall;
+  }
+  // where vector j starts in LDS
+  __device__ __forceinline__ void at(const OrthGroup& g, int j, int& r, int& c) const {
+    const int e = 4 * (64 * j + ((int)threadIdx.x & 63)), q = (int)(((uint32_t)e * g.inv_r) >> 20);
+    r = g.wide ? row + j * rows : q;
+    c = g.wide ? col : e - q * g.r;
+  }
+  // The lane's vectors of a tensor.  FULL (len = g.sub): every vector exists
+  // whole or not at all, and is loaded without a branch (one that does not
+  // exist reads the first and is not used): the compiler waits for a load at
+  // the end of the branch it stands in, so that in branches the loads of a lane
+  // follow one another instead of flying together.
+  template <bool FULL, typename T>
+  __device__ __forceinline__ void load(const OrthGroup& g, const T* p, f32x4 (&x)[kVecs]) const {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if constexpr (FULL) x[j] = load4(p + (valid(g, j) > 0 ? off + j * step : first));
+      else x[j] = load_some(p + off + j * step, valid(g, j));
+    }
+  }
+  template <bool FULL, typename T>
+  __device__ __forceinline__ void store(const OrthGroup& g, T* p, const f32x4 (&x)[kVecs]) const {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      if constexpr (FULL) {
+        if (valid(g, j) > 0) store4(p + off + j * step, x[j]);
+      } else {
+        store_some(p + off + j * step, valid(g, j), x[j]);
+      }
+    }
   }
 };
 // The four elements of a vector that starts at (row, column): a tall one may run over row ends.
@@ -168,79 +206,63 @@ __device__ __forceinline__ f32x4 get4(const OrthGroup& g, const float* lds, int 
   return x;
 }
 
+// U: the gradient, or the momentum form of it.
+enum { ORTH, PLAIN, NESTEROV };
+
 // U of a sub-tile into LDS (zeros past len).  FIRST: the momentum is brought
-// up to date (M <- mu M + G) and stored; later passes read the new one.  All
-// of a lane's loads are issued before the first is waited for.
-template <typename T, bool FIRST>
+// up to date (M <- mu M + G) and stored; later passes read the new one.
+template <typename T, int MODE, bool FIRST, bool FULL>
 __device__ __forceinline__ void load_u(const OrthArgs& a, const OrthGroup& g, const SubTile& st, float* lds) {
-  const T* G = static_cast<const T*>(g.G);
-  const bool need_g = !a.muon || FIRST || a.nesterov;
   f32x4 x[kVecs], m[kVecs];
+  if constexpr (MODE != PLAIN || FIRST) st.load<FULL>(g, static_cast<const T*>(g.G), x);
+  if constexpr (MODE != ORTH) st.load<FULL>(g, static_cast<const float*>(g.M), m);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
-    int valid, row, col;
-    const int64_t o = st.at(g, j, valid, row, col);
-    x[j] = m[j] = f32x4{0, 0, 0, 0};
-    if (need_g) x[j] = load_some(G + o, valid);
-    if (a.muon) m[j] = load_some(g.M + o, valid);
-  }
-#pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    int valid, row, col;
-    const int64_t o = st.at(g, j, valid, row, col);
     f32x4 u = x[j];
-    if (a.muon) {
+    if constexpr (MODE != ORTH)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (FIRST) m[j][i] = fmaf(a.mu, m[j][i], x[j][i]);
-        u[i] = a.nesterov ? fmaf(a.mu, m[j][i], x[j][i]) : m[j][i];
+        u[i] = MODE == NESTEROV ? fmaf(a.mu, m[j][i], x[j][i]) : m[j][i];
       }
-      if (FIRST) store_some(g.M + o, valid, m[j]);
+    int row, col;
+    st.at(g, j, row, col);
+    if (4 * (64 * j + ((int)threadIdx.x & 63)) < st.total) put4(g, lds, row, col, u);
+  }
+  if constexpr (MODE != ORTH && FIRST) st.store<FULL>(g, g.M, m);
+}
+
+// The group of this block, and the block's number within it.
+__device__ __forceinline__ const OrthGroup& my_group(const OrthArgs& a, int launch, int& b) {
+  int k = 0, at = 0;
+#pragma unroll
+  for (int i = 1; i < kMaxGroups; ++i)
+    if ((int)blockIdx.x >= a.first[launch][i]) {
+      k = i;
+      at = a.first[launch][i];
     }
-    if (4 * (64 * j + (int)(threadIdx.x & 63)) < st.total) put4(g, lds, row, col, u);
-  }
+  b = (int)blockIdx.x - at;
+  return a.g[__builtin_amdgcn_readfirstlane(k)];
 }
-
-// The group of block b (first blocks blk0 or mat0 ascending).
-__device__ __forceinline__ int find_group(const OrthArgs& a, int b, bool mats) {
-  int k = 0;
-  for (int i = 1; i < a.ngroups; ++i)
-    if (b >= (mats ? a.g[i].mat0 : a.g[i].blk0)) k = i;
-  return __builtin_amdgcn_readfirstlane(k);
-}
-
-// Where a wavefront of block b works: its group, matrix and chunk, and the
-// sub-tiles of the chunk that are its own.
-struct Place {
-  int mat, chunk;
-  __device__ __forceinline__ Place(const OrthGroup& g, int b) : mat(b / g.chunks), chunk(b % g.chunks) {}
-  __device__ __forceinline__ SubTile sub(const OrthGroup& g, int w, int i) const {
-    const int l0 = ((chunk * 4 + w) * g.nsub + i) * g.sub;
-    SubTile st;
-    st.len = g.n - l0 < g.sub ? g.n - l0 : g.sub;
-    st.total = g.sub * g.r;
-    st.base = (int64_t)mat * g.n * g.r + (g.wide ? (int64_t)l0 : (int64_t)l0 * g.r);
-    return st;
-  }
-};
 
 // Partial U^T U of one matrix over one chunk of its long side.  An operand of
 // tile t holds, in lane 16 q + c, U at long index k + q (any assignment of the
 // four k to the lane groups gives the same sum) and short index NT c + t, and
 // serves as both sides of the product.  Only the tiles on and above the
 // diagonal are formed.  The wavefronts work alone until their sums meet.
-template <typename T, int NT>
-__global__ __launch_bounds__(256) void orth_gram_kernel(const OrthArgs a) {
+template <typename T, int NT, int MODE>
+__global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const OrthArgs a) {
   constexpr int NP = NT * (NT + 1) / 2;
   __shared__ __attribute__((aligned(16))) float us[4][kRegion];
   constexpr int AT = NT == 4 ? 5 : NP;  // tiles whose sums meet at a time, in the regions
   static_assert(sizeof(double) * 3 * AT * 256 <= sizeof(us) && NP % AT == 0, "the exchange fits the regions");
   double* const red = reinterpret_cast<double*>(&us[0][0]);
-  const OrthGroup& g = a.g[find_group(a, blockIdx.x, false)];
+  int b;
+  const OrthGroup& g = my_group(a, GRAM, b);
+  const int mat = b / g.chunks, chunk = b % g.chunks;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
-  const Place at(g, (int)blockIdx.x - g.blk0);
   float* const u = us[w];
   f64x4 acc[NP];
 #pragma unroll
@@ -256,17 +278,20 @@ __global__ __launch_bounds__(256) void orth_gram_kernel(const OrthArgs a) {
       for (int s = t; s < NT; ++s, ++i) acc[i] = __builtin_amdgcn_mfma_f64_16x16x4f64(d[t], d[s], acc[i], 0, 0, 0);
   };
   for (int i = 0; i < g.nsub; ++i) {
-    const SubTile st = at.sub(g, w, i);
+    const SubTile st(g, mat, (chunk * 4 + w) * g.nsub + i);
     if (st.len <= 0) break;
-    load_u<T, true>(a, g, st, u);
+    if (st.len == g.sub) load_u<T, MODE, true, true>(a, g, st, u);
+    else load_u<T, MODE, true, false>(a, g, st, u);
     wave_sync();
     if (!g.wide) {
-#pragma unroll 4
-      for (int k = 0; k < st.len; k += 4) {  // rows up to the sub-tile's (a multiple of 16) are zero past len
-        float x[NT];
+      for (int k = 0; k < st.len; k += 16) {  // rows up to the sub-tile's (a multiple of 16) are zero past len
+        float x[4][NT];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) x[t] = NT * c + t < g.r ? u[(k + q) * g.pitch + NT * c + t] : 0.0f;
-        mma(x);
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) x[v][t] = NT * c + t < g.r ? u[(k + 4 * v + q) * g.pitch + NT * c + t] : 0.0f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) mma(x[v]);
       }
     } else {
       for (int k = 0; k < st.len; k += 16) {
@@ -285,7 +310,7 @@ __global__ __launch_bounds__(256) void orth_gram_kernel(const OrthArgs a) {
     }
     wave_sync();
   }
-  double* out = g.part + ((int64_t)at.mat * g.chunks + at.chunk) * (NP * 256);
+  double* out = g.part + ((int64_t)mat * g.chunks + chunk) * (NP * 256);
 #pragma unroll
   for (int i0 = 0; i0 < NP; i0 += AT) {
     __syncthreads();
@@ -320,8 +345,8 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
   constexpr int N = 16 * NT, LD = N + 2, NP = NT * (NT + 1) / 2, THREADS = NT >= 3 ? 1024 : 256 * NT;
   constexpr int WAVES = THREADS / 64;
   __shared__ double mg[N * LD], mp[N * LD], mv[N * LD], mq[N * LD];
-  const OrthGroup& g = a.g[find_group(a, blockIdx.x, true)];
-  const int mat = (int)blockIdx.x - g.mat0;
+  int mat;
+  const OrthGroup& g = my_group(a, STEPS, mat);
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
@@ -420,38 +445,38 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
   for (int e = threadIdx.x; e < N * N; e += THREADS) Q[e] = mq[e / N * LD + e % N] * inv;
 }
 
-// O = U Q (tall) or Q U (wide) over one chunk of the long side, and its use.
-// A wavefront works alone on each of its sub-tiles: U goes to LDS, 16 rows
+// O = U Q (tall) or Q U (wide) over four sub-tiles, and its use.
+// A wavefront works alone on its sub-tile: U goes to LDS, 16 rows
 // (columns) at a time are multiplied and replaced there by O, which is then
 // read back as it lies in memory for the update of P (loaded with U).
-template <typename T, int NT>
-__global__ __launch_bounds__(256) void orth_apply_kernel(const OrthArgs a) {
+template <typename T, int NT, int MODE>
+__global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_apply_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, S = N / 4;
   __shared__ __attribute__((aligned(16))) float us[4][kRegion];
   __shared__ double mq[N * LD];
-  const OrthGroup& g = a.g[find_group(a, blockIdx.x, false)];
+  int b;
+  const OrthGroup& g = my_group(a, APPLY, b);
+  const int mat = b / g.subs;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, c = lane & 15;
-  const Place at(g, (int)blockIdx.x - g.blk0);
-  const double* Q = g.Q + (int64_t)at.mat * N * N;
-  for (int e = threadIdx.x; e < N * N; e += 256) mq[e / N * LD + e % N] = Q[e];
   T* const P = static_cast<T*>(g.P);
   const double lrs = a.lr * (double)g.scale;
   float* const u = us[w];
-  __syncthreads();
-  for (int i = 0; i < g.nsub; ++i) {
-    const SubTile st = at.sub(g, w, i);
-    if (st.len <= 0) break;
-    f32x4 p[kVecs];
-    if (a.muon)
+  const double* Q = g.Q + (int64_t)mat * N * N;
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        int valid, row, col;
-        const int64_t o = st.at(g, j, valid, row, col);
-        p[j] = load_some(P + o, valid);
-      }
-    load_u<T, false>(a, g, st, u);
+  for (int i = 0; i < N * N / 256; ++i) {
+    const int e = 256 * i + threadIdx.x;
+    mq[e / N * LD + e % N] = Q[e];
+  }
+  __syncthreads();
+  const SubTile st(g, mat, (b % g.subs) * 4 + w);
+  if (st.len <= 0) return;
+  auto body = [&](auto full) {
+    constexpr bool FULL = decltype(full)::value;
+    f32x4 p[kVecs];
+    if constexpr (MODE != ORTH) st.load<FULL>(g, static_cast<const T*>(P), p);
+    load_u<T, MODE, false, FULL>(a, g, st, u);
     wave_sync();
     if (!g.wide) {
       // lane 16 q + c reads row c, short indices S q .. S q + S - 1, and ends with rows 4 v + q,
@@ -506,44 +531,49 @@ __global__ __launch_bounds__(256) void orth_apply_kernel(const OrthArgs a) {
     wave_sync();
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
-      int valid, row, col;
-      const int64_t o = st.at(g, j, valid, row, col);
-      if (valid <= 0) continue;
-      f32x4 x = get4(g, u, row, col);
-      if (a.muon)
+      int row, col;
+      st.at(g, j, row, col);
+      f32x4 o = f32x4{0, 0, 0, 0};
+      if (4 * (64 * j + lane) < st.total) o = get4(g, u, row, col);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) x[v] = (float)fma(a.decay, (double)p[j][v], -lrs * (double)x[v]);
-      store_some(P + o, valid, x);
+      for (int v = 0; v < 4; ++v) p[j][v] = MODE == ORTH ? o[v] : (float)fma(a.decay, (double)p[j][v], -lrs * (double)o[v]);
     }
-    wave_sync();
-  }
+    st.store<FULL>(g, P, p);
+  };
+  if (st.len == g.sub) body(std::true_type{});
+  else body(std::false_type{});
 }
 
-template <typename T, int NT>
-hipError_t launch_orth(const OrthArgs& a, int blocks, int mats, hipStream_t st) {
+template <typename T, int NT, int MODE>
+hipError_t launch_orth(const OrthArgs& a, const int64_t (&blocks)[3], hipStream_t st) {
   {
     TraceScope ts("orth_gram", st);
-    hipLaunchKernelGGL((orth_gram_kernel<T, NT>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((orth_gram_kernel<T, NT, MODE>), dim3((unsigned)blocks[GRAM]), dim3(256), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   {
     TraceScope ts("orth_steps", st);
-    hipLaunchKernelGGL((orth_steps_kernel<NT>), dim3((unsigned)mats), dim3(NT >= 3 ? 1024 : 256 * NT), 0, st, a);
+    hipLaunchKernelGGL((orth_steps_kernel<NT>), dim3((unsigned)blocks[STEPS]), dim3(NT >= 3 ? 1024 : 256 * NT), 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   TraceScope ts("orth_apply", st);
-  hipLaunchKernelGGL((orth_apply_kernel<T, NT>), dim3((unsigned)blocks), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((orth_apply_kernel<T, NT, MODE>), dim3((unsigned)blocks[APPLY]), dim3(256), 0, st, a);
   return hipGetLastError();
 }
+template <typename T, int NT>
+hipError_t launch_orth_mode(int mode, const OrthArgs& a, const int64_t (&blocks)[3], hipStream_t st) {
+  return mode == ORTH ? launch_orth<T, NT, ORTH>(a, blocks, st)
+                      : mode == PLAIN ? launch_orth<T, NT, PLAIN>(a, blocks, st) : launch_orth<T, NT, NESTEROV>(a, blocks, st);
+}
 template <typename T>
-hipError_t launch_orth_nt(int nt, const OrthArgs& a, int blocks, int mats, hipStream_t st) {
+hipError_t launch_orth_nt(int nt, int mode, const OrthArgs& a, const int64_t (&blocks)[3], hipStream_t st) {
   switch (nt) {
-    case 1: return launch_orth<T, 1>(a, blocks, mats, st);
-    case 2: return launch_orth<T, 2>(a, blocks, mats, st);
-    case 3: return launch_orth<T, 3>(a, blocks, mats, st);
-    default: return launch_orth<T, 4>(a, blocks, mats, st);
+    case 1: return launch_orth_mode<T, 1>(mode, a, blocks, st);
+    case 2: return launch_orth_mode<T, 2>(mode, a, blocks, st);
+    case 3: return launch_orth_mode<T, 3>(mode, a, blocks, st);
+    default: return launch_orth_mode<T, 4>(mode, a, blocks, st);
   }
 }
 
@@ -555,7 +585,8 @@ struct Shape {
   int32_t sub, sub_log2, pitch, nsub;
   size_t part, q;  // workspace bytes
 };
-Shape shape_of(const lora_orth_mat& m) {
+// most: sub-tiles per wavefront of a block that forms U^T U, at most
+Shape shape_of(const lora_orth_mat& m, int most = 4) {
   Shape s;
   s.n = m.rows > m.cols ? m.rows : m.cols;
   s.r = m.rows > m.cols ? m.cols : m.rows;
@@ -574,11 +605,22 @@ Shape shape_of(const lora_orth_mat& m) {
     s.sub = (int32_t)std::min<int64_t>(256, std::min(kSub / s.r, 2560 / (int64_t)s.pitch) / 16 * 16);
   }
   // more sub-tiles per block where a partial Gram matrix is larger
-  s.nsub = (int32_t)s.nt;
+  s.nsub = (int32_t)std::min<int64_t>(s.nt, most);
   s.chunks = cdiv(s.n, (int64_t)4 * s.sub * s.nsub);
   s.part = (size_t)(m.count * s.chunks * (s.nt * (s.nt + 1) / 2) * 256 * 8);
   s.q = (size_t)(m.count * s.nt * s.nt * 256 * 8);
   return s;
+}
+
+// Fewer sub-tiles a block where the call would not fill the chip.
+int most_sub_tiles(const lora_orth_desc* d, const lora_orth_mat* mats) {
+  int most = 4;
+  for (; most > 1; most /= 2) {
+    int64_t blocks = 0;
+    for (int i = 0; i < d->n && blocks < 256; ++i) blocks += mats[i].count * shape_of(mats[i], most).chunks;
+    if (blocks >= 256) break;
+  }
+  return most;
 }
 
 lora_status check_orth(const lora_orth_desc* d, const lora_orth_mat* mats) {
@@ -595,7 +637,7 @@ lora_status check_orth(const lora_orth_desc* d, const lora_orth_mat* mats) {
           (long long)m.rows, (long long)m.cols);
     CHECK(m.rows <= 64 || m.cols <= 64, LORA_ESHAPE, "mats[%d]: neither side of [%lld, %lld] is at most 64", i,
           (long long)m.rows, (long long)m.cols);
-    const Shape s = shape_of(m);
+    const Shape s = shape_of(m, 1);
     CHECK(s.n < ((int64_t)1 << 30) && m.count <= ((int64_t)1 << 30) / s.chunks, LORA_ESHAPE,
           "mats[%d]: %lld x [%lld, %lld] is too large", i, (long long)m.count, (long long)m.rows, (long long)m.cols);
     CHECK(m.reserved == 0, LORA_EINVAL, "mats[%d].reserved must be 0", i);
@@ -605,8 +647,9 @@ lora_status check_orth(const lora_orth_desc* d, const lora_orth_mat* mats) {
 
 size_t orth_bytes(const lora_orth_desc* d, const lora_orth_mat* mats) {
   Ws w(nullptr);
+  const int most = most_sub_tiles(d, mats);
   for (int i = 0; i < d->n; ++i) {
-    const Shape s = shape_of(mats[i]);
+    const Shape s = shape_of(mats[i], most);
     w.take(s.part);
     w.take(s.q);
   }
@@ -655,32 +698,40 @@ lora_status check_mats(const lora_orth_desc* d, const lora_orth_mat* mats, bool 
   return LORA_OK;
 }
 
-lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, OrthArgs a, void* ws, hipStream_t st) {
+lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, int mode, OrthArgs a, void* ws, hipStream_t st) {
   a.steps = d->steps;
   a.a = d->a;
   a.b = d->b;
   a.c = d->c;
   a.eps = d->eps;
   // one set of three launches for all stacks with the same number of tiles, kMaxGroups at a time
+  const int most = most_sub_tiles(d, mats);
   for (int nt = 1; nt <= 4; ++nt) {
-    int64_t blocks = 0, nmat = 0;
+    int64_t blocks[3] = {0, 0, 0};
     a.ngroups = 0;
     Ws w(ws);
     auto flush = [&]() -> hipError_t {
       if (a.ngroups == 0) return hipSuccess;
-      const hipError_t e = d->dtype == LORA_F32 ? launch_orth_nt<float>(nt, a, (int)blocks, (int)nmat, st)
-                                                : launch_orth_nt<uint16_t>(nt, a, (int)blocks, (int)nmat, st);
+      for (int k = 0; k < 3; ++k)
+        for (int i = a.ngroups; i < kMaxGroups; ++i) a.first[k][i] = INT32_MAX;
+      const hipError_t e = d->dtype == LORA_F32 ? launch_orth_nt<float>(nt, mode, a, blocks, st)
+                                                : launch_orth_nt<uint16_t>(nt, mode, a, blocks, st);
       a.ngroups = 0;
-      blocks = nmat = 0;
+      blocks[GRAM] = blocks[STEPS] = blocks[APPLY] = 0;
       return e;
     };
     for (int i = 0; i < d->n; ++i) {
       const lora_orth_mat& m = mats[i];
-      const Shape s = shape_of(m);
+      const Shape s = shape_of(m, most);
+      const int64_t subs = cdiv(s.n, 4 * s.sub), add[3] = {m.count * s.chunks, m.count, m.count * subs};
       double* part = static_cast<double*>(w.take(s.part));
       double* Q = static_cast<double*>(w.take(s.q));
       if (s.nt != nt || m.count == 0) continue;
-      if (a.ngroups == kMaxGroups || blocks + m.count * s.chunks > ((int64_t)1 << 30)) LAUNCH(flush());
+      if (a.ngroups == kMaxGroups || blocks[APPLY] + add[APPLY] > ((int64_t)1 << 30)) LAUNCH(flush());
+      for (int k = 0; k < 3; ++k) {
+        a.first[k][a.ngroups] = (int32_t)blocks[k];
+        blocks[k] += add[k];
+      }
       OrthGroup& g = a.g[a.ngroups++];
       g.wide = m.cols > m.rows;
       g.G = m.G;
@@ -690,7 +741,6 @@ lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, OrthArg
       g.Q = Q;
       g.n = (int32_t)s.n;
       g.r = (int32_t)s.r;
-      g.count = (int32_t)m.count;
       g.chunks = (int32_t)s.chunks;
       g.sub = s.sub;
       g.sub_log2 = s.sub_log2;
@@ -698,11 +748,8 @@ lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, OrthArg
       g.nsub = s.nsub;
       g.inv_r = (uint32_t)cdiv((int64_t)1 << 20, s.r);
       g.vec_lds = g.wide || s.r % 4 == 0;
-      g.blk0 = (int32_t)blocks;
-      g.mat0 = (int32_t)nmat;
+      g.subs = (int32_t)subs;
       g.scale = m.scale;
-      blocks += m.count * s.chunks;
-      nmat += m.count;
     }
     LAUNCH(flush());
   }
@@ -728,7 +775,7 @@ lora_status lora_orthogonalize(const lora_orth_desc* d, const lora_orth_mat* mat
   TRY(check_ws(ws, ws_bytes, need));
   TRY(check_mats(d, mats, false, ws, need));
   OrthArgs a{};
-  return run_orth(d, mats, a, ws, static_cast<hipStream_t>(stream));
+  return run_orth(d, mats, ORTH, a, ws, static_cast<hipStream_t>(stream));
 }
 
 lora_status lora_muon_step(const lora_muon_desc* d, const lora_orth_mat* mats, void* ws, size_t ws_bytes, void* stream) {
@@ -742,12 +789,10 @@ lora_status lora_muon_step(const lora_muon_desc* d, const lora_orth_mat* mats, v
   TRY(check_ws(ws, ws_bytes, need));
   TRY(check_mats(&d->orth, mats, true, ws, need));
   OrthArgs a{};
-  a.muon = 1;
-  a.nesterov = d->nesterov;
   a.mu = (float)d->momentum;
   a.lr = d->lr;
   a.decay = 1.0 - d->lr * d->weight_decay;
-  return run_orth(&d->orth, mats, a, ws, static_cast<hipStream_t>(stream));
+  return run_orth(&d->orth, mats, d->nesterov ? NESTEROV : PLAIN, a, ws, static_cast<hipStream_t>(stream));
 }
 
 }  // extern "C"
