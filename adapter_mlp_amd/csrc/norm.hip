@@ -11,6 +11,7 @@
 // read once; the row sums are the only exchange between threads.  Sums,
 // norms and everything between a load and a store are fp32: X is formed from
 // the unrounded R', so each output carries one rounding.
+#include <algorithm>
 #include <cmath>
 
 #include "abi.hpp"
@@ -113,11 +114,24 @@ constexpr int norm_block() {
   return TPR < 256 ? 256 : TPR;
 }
 
+// What fits the registers: a block of 1024 threads has 128 a thread, fewer
+// threads 256 and two blocks a CU.  PREFETCH: the next row's operands are
+// loaded before this row's sums are waited for.  KEEP: the weights stay in
+// registers instead of being read again (from L2) for every row.
+template <typename TA, int VEC, int TPR, int NV>
+constexpr bool norm_prefetch(bool bwd) {
+  return bwd ? (VEC * NV <= 16 && TPR < 1024 && (sizeof(TA) == 2 || VEC * NV == 8)) : (TPR < 1024 || sizeof(TA) == 2);
+}
+template <typename TA, int VEC, int TPR, int NV>
+constexpr bool norm_keep(bool bwd) {
+  return norm_prefetch<TA, VEC, TPR, NV>(bwd);
+}
+
 // Thread tx of a row's TPR threads owns the vectors tx, tx + TPR, ... (NV of
-// them) in every row it meets, so the weights stay in its registers, and the
-// next row's operands are loaded before this row's sums are waited for.
+// them) in every row it meets.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormArgs a) {
+  constexpr bool PREFETCH = norm_prefetch<TA, VEC, TPR, NV>(false), KEEP = norm_keep<TA, VEC, TPR, NV>(false);
   __shared__ float lds[2][1][TPR / 64];
   constexpr int RPB = norm_block<TPR>() / TPR;
   const int tx = threadIdx.x % TPR;
@@ -129,16 +143,20 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
   bool ok[NV];
   Vec<TP, VEC> wq[NV], wp[NV], gc[NV];
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * TPR + tx) * VEC;
-    ok[v] = c < H;
-    wq[v].zero();
-    wp[v].zero();
-    gc[v].zero();
-    if (ok[v] && post) wq[v].load(a.w_post, c);
-    if (ok[v] && pre) wp[v].load(a.w_pre, c);
-    if (ok[v] && gate == GATE_COL) gc[v].load(a.g, c);
-  }
+  for (int v = 0; v < NV; ++v) ok[v] = (v * TPR + tx) * VEC < H;
+  auto weights = [&]() {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + tx) * VEC;
+      wq[v].zero();
+      wp[v].zero();
+      gc[v].zero();
+      if (ok[v] && post) wq[v].load(a.w_post, c);
+      if (ok[v] && pre) wp[v].load(a.w_pre, c);
+      if (ok[v] && gate == GATE_COL) gc[v].load(a.g, c);
+    }
+  };
+  if constexpr (KEEP) weights();
   Vec<TA, VEC> nr[NV], ny[NV], ng[NV];
   const int64_t step = (int64_t)gridDim.x * RPB;
   auto fetch = [&](int64_t t) {
@@ -156,8 +174,10 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
     }
   };
   int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  fetch(t);
+  if constexpr (PREFETCH) fetch(t);
   for (; t < a.T; t += step) {
+    if constexpr (!PREFETCH) fetch(t);
+    if constexpr (!KEEP) weights();
     Vec<TA, VEC> r[NV], y[NV], ge[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -165,7 +185,7 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
       y[v] = ny[v];
       ge[v] = ng[v];
     }
-    fetch(t + step);
+    if constexpr (PREFETCH) fetch(t + step);
     float s[NV * VEC];
     if (branch) {
       float u = 1.0f;
@@ -227,7 +247,8 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
 // registers of the thread that owns the column, one slice per block, and
 // norm_grad_kernel adds the slices in ascending order.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
-__global__ __launch_bounds__(norm_block<TPR>()) void norm_bwd_kernel(const NormArgs a) {
+__global__ __launch_bounds__(norm_block<TPR>(), TPR <= 256 ? 2 : 1) void norm_bwd_kernel(const NormArgs a) {
+  constexpr bool PREFETCH = norm_prefetch<TA, VEC, TPR, NV>(true), KEEP = norm_keep<TA, VEC, TPR, NV>(true);
   constexpr int RPB = norm_block<TPR>() / TPR;
   constexpr int E = NV * VEC;
   __shared__ float lds3[2][3][TPR / 64];
@@ -246,37 +267,57 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_bwd_kernel(const NormA
 #pragma unroll
   for (int e = 0; e < E; ++e) acc_pre[e] = acc_post[e] = acc_gate[e] = 0.0f;
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int c = (v * TPR + tx) * VEC;
-    ok[v] = c < H;
-    wq[v].zero();
-    wp[v].zero();
-    gc[v].zero();
-    if (ok[v] && post) wq[v].load(a.w_post, c);
-    if (ok[v] && pre) wp[v].load(a.w_pre, c);
-    if (ok[v] && gate == GATE_COL) gc[v].load(a.g, c);
-  }
+  for (int v = 0; v < NV; ++v) ok[v] = (v * TPR + tx) * VEC < H;
+  auto weights = [&]() {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TPR + tx) * VEC;
+      wq[v].zero();
+      wp[v].zero();
+      gc[v].zero();
+      if (ok[v] && post) wq[v].load(a.w_post, c);
+      if (ok[v] && pre) wp[v].load(a.w_pre, c);
+      if (ok[v] && gate == GATE_COL) gc[v].load(a.g, c);
+    }
+  };
+  if constexpr (KEEP) weights();
   const int64_t step = (int64_t)gridDim.x * RPB;
-  for (int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR; t < a.T; t += step) {
-    Vec<TA, VEC> o[NV], dx[NV], dr[NV], y[NV], ge[NV];
+  Vec<TA, VEC> no[NV], ndx[NV], ndr[NV], ny[NV], nge[NV];  // the next row's operands
+  auto fetch = [&](int64_t t) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t i = t * H + (v * TPR + tx) * VEC;
-      o[v].zero();
-      dx[v].zero();
-      dr[v].zero();
-      y[v].zero();
-      ge[v].zero();
-      if (ok[v]) {
+      no[v].zero();
+      ndx[v].zero();
+      ndr[v].zero();
+      ny[v].zero();
+      nge[v].zero();
+      if (ok[v] && t < a.T) {
         if (pre) {
-          o[v].load(a.R, i);
-          dx[v].load(a.dX, i);
+          no[v].load(a.R, i);
+          ndx[v].load(a.dX, i);
         }
-        if (need_y) y[v].load(a.Y, i);
-        if (has_dr) dr[v].load(a.dR, i);
-        if (gate == GATE_ELEM) ge[v].load(a.g, i);
+        if (need_y) ny[v].load(a.Y, i);
+        if (has_dr) ndr[v].load(a.dR, i);
+        if (gate == GATE_ELEM) nge[v].load(a.g, i);
       }
     }
+  };
+  int64_t t = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+  if constexpr (PREFETCH) fetch(t);
+  for (; t < a.T; t += step) {
+    if constexpr (!PREFETCH) fetch(t);
+    if constexpr (!KEEP) weights();
+    Vec<TA, VEC> o[NV], dx[NV], dr[NV], y[NV], ge[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      o[v] = no[v];
+      dx[v] = ndx[v];
+      dr[v] = ndr[v];
+      y[v] = ny[v];
+      ge[v] = nge[v];
+    }
+    if constexpr (PREFETCH) fetch(t + step);
     float uo = 0.0f, mo = 0.0f, uy = 1.0f;
     if (pre || post) {
       float q[3] = {0.0f, 0.0f, 0.0f};
@@ -415,8 +456,7 @@ int64_t bwd_blocks(int64_t T, int64_t H) {
   return need < 512 ? need : 512;
 }
 
-// Threads per row and vectors per thread: the smallest that hold the row,
-// with 8 or 16 elements a thread.
+// Threads per row and elements per thread: the smallest that hold the row.
 template <bool BWD, typename TA, typename TP, int VEC, int TPR, int E>
 hipError_t launch_cfg(const NormArgs& a, hipStream_t st) {
   constexpr int B = norm_block<TPR>(), RPB = B / TPR;
@@ -424,7 +464,7 @@ hipError_t launch_cfg(const NormArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((norm_bwd_kernel<TA, TP, VEC, TPR, E / VEC>), dim3((unsigned)bwd_blocks(a.T, a.H)), dim3(B), 0, st,
                        a);
   } else {
-    const int64_t need = cdiv(a.T, RPB), cap = 256 * (2048 / B);
+    const int64_t need = cdiv(a.T, RPB), cap = 256 * std::max(2048 / B, 4);
     hipLaunchKernelGGL((norm_fwd_kernel<TA, TP, VEC, TPR, E / VEC>), dim3((unsigned)(need < cap ? need : cap)), dim3(B), 0,
                        st, a);
   }
@@ -435,9 +475,20 @@ hipError_t launch_vec(const NormArgs& a, hipStream_t st) {
   if (a.H <= 512) return launch_cfg<BWD, TA, TP, VEC, 64, 8>(a, st);
   if (a.H <= 1024) return launch_cfg<BWD, TA, TP, VEC, 64, 16>(a, st);
   if (a.H <= 2048) return launch_cfg<BWD, TA, TP, VEC, 256, 8>(a, st);
-  if (a.H <= 4096) return launch_cfg<BWD, TA, TP, VEC, 256, 16>(a, st);
+  if constexpr (VEC == 1) {  // sixteen scalars of each operand do not fit the registers of a backward pass
+    if (a.H <= 4096) return launch_cfg<BWD, TA, TP, VEC, 512, 8>(a, st);
+  } else {
+    if (a.H <= 4096) return launch_cfg<BWD, TA, TP, VEC, 256, 16>(a, st);
+  }
+  if constexpr (VEC == 8) {  // rows of 5120: 61 us forward with 512 threads of 16 elements, 51 us so
+    if (a.H <= 5120) return launch_cfg<BWD, TA, TP, VEC, 640, 8>(a, st);
+    if (a.H <= 6144) return launch_cfg<BWD, TA, TP, VEC, 768, 8>(a, st);
+  }
   if (a.H <= 8192) return launch_cfg<BWD, TA, TP, VEC, 512, 16>(a, st);
-  return launch_cfg<BWD, TA, TP, VEC, 1024, 16>(a, st);
+  // a bf16 backward's sums spill less from 512 threads of 32 elements than from 1024 of 16, which
+  // have 128 registers each (250 against 336 us at 2048 rows of 16384)
+  if constexpr (BWD && VEC == 8) return launch_cfg<BWD, TA, TP, VEC, 512, 32>(a, st);
+  else return launch_cfg<BWD, TA, TP, VEC, 1024, 16>(a, st);
 }
 template <bool BWD>
 hipError_t launch_norm(const NormArgs& a, int32_t dtype, bool vec, hipStream_t st) {
