@@ -19,7 +19,7 @@ struct MultiArgs {
   float* part;   // [ks, T, N] fp32 sums of X W over K ranges (nullptr: add to Y)
   float* upart;  // [kc, T, r] fp32 sums of X A_i over K ranges
   int64_t T, K, N, n;
-  int32_t r, ks, kc, ntn;
+  int32_t r, ks, kc, ntn, ntm;
   int32_t nshrink, nz;  // few rows: blocks of the shrink, and how many share the adapters of 16 rows
   uint16_t* u;       // [T, 64] bf16: scaled U, zero past the rank (many rows)
   MultiTile* plan;   // adapters of every 256-row tile (many rows)
@@ -77,15 +77,19 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = w & 1, kh = w >> 1;
-  const int tn = bid % a.ntn, part = bid / a.ntn;
+  // blocks b, b + 8, ... run on one XCD: the row tiles of one part of W follow each other there
+  const int j = bid >> 3, unit = (j / a.ntm) * 8 + (bid & 7), tm = j % a.ntm;
+  if (unit >= a.ntn * a.ks) return;
+  const int tn = unit % a.ntn, part = unit / a.ntn;
   const int steps = (int)(a.K / 64);
   const int s0 = (int)((int64_t)part * steps / a.ks), s1 = (int)((int64_t)(part + 1) * steps / a.ks);
   const int64_t n0 = (int64_t)tn * 128;
   const uint32_t ldw2 = (uint32_t)(a.N * 2), ldx2 = (uint32_t)(a.K * 2);
   const char* wp = static_cast<const char*>(a.W) + ((int64_t)s0 * 64 * a.N + n0) * 2;
   int64_t wn = ((a.K - (int64_t)s0 * 64) * a.N - n0) * 2;
-  const char* xp = static_cast<const char*>(a.X) + (int64_t)s0 * 128;
-  int64_t xn = (a.T * a.K - (int64_t)s0 * 64) * 2;
+  const int64_t m0 = (int64_t)tm * (16 * MT);
+  const char* xp = static_cast<const char*>(a.X) + (m0 * a.K + (int64_t)s0 * 64) * 2;
+  int64_t xn = ((a.T - m0) * a.K - (int64_t)s0 * 64) * 2;
   const uint32_t woff = (uint32_t)(lane >> 4) * ldw2 + (uint32_t)(((lane & 15) ^ (4 * ((lane >> 4) & 3))) * 16);
   // X block b of 1 KB holds rows 8 b .. 8 b + 7; wavefront w loads blocks w, w + 4, ... of 2 MT
   constexpr int XP = (2 * MT + 3) / 4;
@@ -93,7 +97,7 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
 #pragma unroll
   for (int i = 0; i < XP; ++i) {
     const int row = 8 * (w + 4 * i) + (lane >> 3);
-    xoff[i] = row < a.T ? (uint32_t)row * ldx2 + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16) : 0x80000000u;
+    xoff[i] = m0 + row < a.T ? (uint32_t)row * ldx2 + (uint32_t)(((lane & 7) ^ (lane >> 3)) * 16) : 0x80000000u;
   }
   auto issue = [&](int slot) {
     const uint32_t base = lds_addr(lds) + slot * C::SB;
@@ -159,7 +163,7 @@ __device__ __forceinline__ void base_block(const MultiArgs& a, char* ring, int b
     float* out = a.part + (int64_t)part * a.T * a.N;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int64_t t = 16 * m + c;
+      const int64_t t = m0 + 16 * m + c;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t col = n0 + 64 * h + 16 * i + 4 * g;
@@ -280,8 +284,15 @@ __device__ __forceinline__ void shrink_few_block(const MultiArgs& a, char* lds, 
   }
 }
 
-// Both in one launch, which neither waits for the other in: blocks 0 ..
-// nshrink - 1 form U (first, since they are short), the rest X W.
+template <int NJ>
+__global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a) {
+  __shared__ __attribute__((aligned(16))) char lds[3 * NJ * 1024];
+  const int b = blockIdx.x, kz = b % (a.kc * a.nz);
+  shrink_few_block<NJ>(a, lds, b / (a.kc * a.nz), kz / a.nz, kz % a.nz, a.nz);
+}
+
+// X W, and where nshrink > 0 U beside it in the same launch, neither waiting
+// for the other: blocks 0 .. nshrink - 1 form U (first, since they are short).
 template <int MT>
 __global__ __launch_bounds__(256, BaseCfg<MT>::PER_CU) void multi_few_kernel(const MultiArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[BaseCfg<MT>::SMEM];
@@ -720,17 +731,34 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
 // ---------------------------------------------------------------------------
 // Launches.
 // ---------------------------------------------------------------------------
-// bf16 calls of up to kFewRows rows stream W in one row tile (16 rows and up)
-// and add the adapters to the fp32 sums; beyond that the 256 x 256 tiles of
-// the GEMM take over, with the adapters in its epilogue.
+// Which path a bf16 call takes.  Few rows: W is streamed through 128-column
+// tiles with K split over the grid, and the adapters join the fp32 sums as
+// those are added up.  Many: the 256 x 256 tiles of the GEMM, with the adapters
+// in its epilogue.  Fitted to both, timed from 130 to 1024 rows (rank 16 to 64;
+// us, few / many):
+//    4096 x 4096: 30 / 61 at 130 rows, 53 / 62 at 512, 72 / 64 at 640
+//    4096 x 14336: 44 / 67 at 130, 71 / 74 at 256, 101 / 85 at 300
+//    14336 x 4096: 54 / 103 at 130, 108 / 111 at 300, 120 / 107 at 384
+//    4096 x 1024: 57 / 55 at 1024;  640 x 640: 26 / 40 at 1024
+// few takes about T K N / 3e8 + T K / 1.9e5 + 16 us, many T K N / 1.1e9 +
+// K / 213 + 38 us; up to kFewRows rows always, and past 1024 never.
 constexpr int64_t kFewRows = 128;
+bool few_rows(int64_t T, int64_t K, int64_t N) {
+  if (T <= kFewRows || T > 1024) return T <= kFewRows;
+  const double t = (double)T, k = (double)K;
+  return t * k * ((double)N / 4.1e8 + 1 / 1.9e5) < 0.85 * (22 + k / 213);
+}
+
+// Row tiles of at most 128 rows, and the 16-row blocks of each.
+int row_tiles(int64_t T) { return (int)cdiv(T, 128); }
+int row_blocks(int64_t T) { return (int)cdiv(cdiv(T, 16), row_tiles(T)); }
 
 // K ranges of the shrink.
-int shrink_ranges(int64_t T, int64_t K) { return (int)cdiv(K, T > kFewRows ? kShrinkK : 4 * kShrinkK); }
+int shrink_ranges(bool few, int64_t K) { return (int)cdiv(K, few ? 4 * kShrinkK : kShrinkK); }
 // Few rows: 16 of them meet at most 16 adapters, each in a block of its own.
 int shrink_share(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(16, n)); }
 int shrink_blocks(int64_t T, int64_t K, int64_t n) {
-  return n == 0 ? 0 : (int)cdiv(T, 16) * shrink_ranges(T, K) * shrink_share(n);
+  return n == 0 ? 0 : (int)cdiv(T, 16) * shrink_ranges(true, K) * shrink_share(n);
 }
 
 // K ranges of X W for few rows, by a model of the grid: rounds of the blocks
@@ -739,8 +767,8 @@ int shrink_blocks(int64_t T, int64_t K, int64_t n) {
 // written and read again, and the shrink's 4 us where its blocks find no room
 // beside the others.
 int base_ksplit(int64_t T, int64_t K, int64_t N, int shrink) {
-  const int mt = (int)cdiv(T, 16), per_cu = mt <= 5 ? 2 : 1;
-  const int64_t units = cdiv(N, 128), steps = K / 64;
+  const int mt = row_blocks(T), per_cu = mt <= 5 ? 2 : 1;
+  const int64_t units = cdiv(N, 128) * row_tiles(T), steps = K / 64;
   double best = 0.0;
   int bs = 1;
   for (int s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
@@ -755,15 +783,25 @@ int base_ksplit(int64_t T, int64_t K, int64_t N, int shrink) {
   return bs;
 }
 
+hipError_t launch_shrink_few(const MultiArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)a.nshrink);
+  switch (cdiv(a.r, 16)) {
+    case 1: hipLaunchKernelGGL(multi_shrink_few_kernel<1>, grid, dim3(256), 0, st, a); break;
+    case 2: hipLaunchKernelGGL(multi_shrink_few_kernel<2>, grid, dim3(256), 0, st, a); break;
+    case 3: hipLaunchKernelGGL(multi_shrink_few_kernel<3>, grid, dim3(256), 0, st, a); break;
+    default: hipLaunchKernelGGL(multi_shrink_few_kernel<4>, grid, dim3(256), 0, st, a); break;
+  }
+  return hipGetLastError();
+}
 template <int MT>
 hipError_t launch_few(const MultiArgs& a, hipStream_t st) {
-  const int blocks = a.nshrink + (a.W ? a.ntn * a.ks : 0);
+  const int blocks = a.nshrink + (a.W ? (int)cdiv(a.ntn * a.ks, 8) * 8 * a.ntm : 0);
   if (blocks == 0) return hipSuccess;
   hipLaunchKernelGGL(multi_few_kernel<MT>, dim3((unsigned)blocks), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 hipError_t launch_few_mt(const MultiArgs& a, hipStream_t st) {
-  switch (cdiv(a.T, 16)) {
+  switch (row_blocks(a.T)) {
     case 1: return launch_few<1>(a, st);
     case 2: return launch_few<2>(a, st);
     case 3: return launch_few<3>(a, st);
@@ -789,6 +827,7 @@ hipError_t launch_shrink(const MultiArgs& a, hipStream_t st) {
 
 // Workspace of a call.
 struct MultiPlan {
+  bool few;    // the path of few rows
   bool tiles;  // the GEMM path
   int ks, kc;
   float *part, *upart;
@@ -799,14 +838,15 @@ struct MultiPlan {
 MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   MultiPlan p{};
   const bool bf16 = d.dtype == LORA_BF16;
-  p.tiles = bf16 && base && d.T > kFewRows;
+  p.few = base ? few_rows(d.T, d.K, d.N) : d.T <= kFewRows;
+  p.tiles = bf16 && base && !p.few;
   p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K)
                                               : base_ksplit(d.T, d.K, d.N, shrink_blocks(d.T, d.K, d.n));
-  p.kc = bf16 ? shrink_ranges(d.T, d.K) : 1;
+  p.kc = bf16 ? shrink_ranges(p.few, d.K) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
   if (p.tiles) p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
-  if (bf16 && d.T > kFewRows) {
+  if (bf16 && !p.few) {
     p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
   }
   if (bf16 && base && (!p.tiles || p.ks > 1)) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
@@ -895,9 +935,16 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   a.u = p.u;
   a.plan = p.plan;
   if (bf16) {
-    if (d->T <= kFewRows) {
+    if (p.few) {
+      a.ntm = row_tiles(d->T);
       a.nz = shrink_share(d->n);
       a.nshrink = shrink_blocks(d->T, d->K, d->n);
+      // one launch saves a few us; but the shrink's blocks then take the LDS of the others, which
+      // many of them would wait for
+      if (d->T > kFewRows && a.nshrink > 0) {
+        LAUNCHN("multi_shrink_few", st, launch_shrink_few(a, st));
+        a.nshrink = 0;
+      }
       LAUNCHN("multi_few", st, launch_few_mt(a, st));
     } else if (p.tiles || d->n > 0) {  // without adapters the GEMM's tiles are still listed, as empty
       LAUNCHN("multi_shrink", st, launch_shrink(a, st));

@@ -72,7 +72,8 @@ def run(s, **kw):
 
 CASES = [(1, 64, 64, 8, 1), (1, 4096, 1024, 16, 3), (2, 128, 192, 16, 5), (16, 320, 576, 24, 7), (17, 1024, 128, 32, 40),
          (33, 1088, 704, 40, 4), (64, 512, 1024, 48, 9), (65, 4096, 512, 64, 80), (129, 2112, 320, 56, 6), (300, 576, 1088, 8, 300),
-         (777, 1024, 640, 16, 12), (1030, 256, 2048, 64, 3), (2500, 512, 512, 32, 20)]
+         (777, 1024, 640, 16, 12), (1030, 256, 2048, 64, 3), (2500, 512, 512, 32, 20),
+         (1300, 640, 320, 40, 300), (450, 4096, 4160, 16, 5), (1025, 64, 64, 8, 1), (1800, 192, 448, 56, 70)]
 
 
 @pytest.mark.gpu
@@ -118,7 +119,7 @@ def test_beside_an_nf4_base():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 40, 900])
+@pytest.mark.parametrize("T", [1, 40, 900, 1100])
 def test_one_adapter_agrees_with_o_fwd(T):
     s = make(T, 512, 768, 16, 3, ids="one")
     p = s["pool"]
@@ -128,7 +129,7 @@ def test_one_adapter_agrees_with_o_fwd(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [9, 80, 1000])
+@pytest.mark.parametrize("T", [9, 80, 1000, 1200])
 def test_a_bad_adapter_or_row_stays_alone(T):
     s = make(T, 512, 512, 24, 8)
     want = run(s)
@@ -152,7 +153,7 @@ def test_no_rows_and_no_adapters(dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [5, 100, 1500])
+@pytest.mark.parametrize("T", [5, 100, 600, 1500])
 def test_other_stream_and_same_answer(T):
     s = make(T, 1024, 1024, 16, 7)
     want = run(s)
@@ -166,7 +167,7 @@ def test_other_stream_and_same_answer(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [3, 90, 1300])
+@pytest.mark.parametrize("T", [3, 90, 500, 1300])
 def test_captured_graph_replays(T):
     s = make(T, 512, 576, 16, 6)
     Y = run(s)
@@ -185,7 +186,7 @@ def test_captured_graph_replays(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("T", [4, 700, 1100])
 def test_stacks_past_two_gib(T):
     s = make(T, 64, 128, 64, 2, ids="each")
     n = 1 << 18
