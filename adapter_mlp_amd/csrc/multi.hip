@@ -330,15 +330,27 @@ __device__ __forceinline__ void sort_tile(int id, int* keys, int* id_of, int* ro
   const int key = id < 0 ? 0x7fffffff : id;
   keys[i] = key;
   __syncthreads();
+  // keys before this one, equal keys in the order of their rows: smaller or equal among the
+  // wavefronts before, smaller among those after, and by row within its own
   int rank = 0;
   const int4* k4 = reinterpret_cast<const int4*>(keys);
+  const int w = __builtin_amdgcn_readfirstlane(i >> 6);
 #pragma unroll 16
-  for (int j = 0; j < 64; ++j) {
+  for (int j = 0; j < 16 * w; ++j) {
     const int4 k = k4[j];
-    // equal keys keep their order
+    rank += (int)(k.x <= key) + (int)(k.y <= key) + (int)(k.z <= key) + (int)(k.w <= key);
+  }
+#pragma unroll
+  for (int j = 16 * w; j < 16 * w + 16; ++j) {
+    const int4 k = k4[j];
     rank += (int)(k.x < key) + (int)(k.y < key) + (int)(k.z < key) + (int)(k.w < key);
     rank += ((int)(k.x == key) & (int)(4 * j < i)) + ((int)(k.y == key) & (int)(4 * j + 1 < i)) +
             ((int)(k.z == key) & (int)(4 * j + 2 < i)) + ((int)(k.w == key) & (int)(4 * j + 3 < i));
+  }
+#pragma unroll 16
+  for (int j = 16 * w + 16; j < 64; ++j) {
+    const int4 k = k4[j];
+    rank += (int)(k.x < key) + (int)(k.y < key) + (int)(k.z < key) + (int)(k.w < key);
   }
   id_of[rank] = id;
   row_of[rank] = i;
@@ -452,27 +464,39 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
 }
 
 // U of many rows as the GEMM reads it: summed over the K ranges, scaled and
-// rounded to bf16 (as the one-adapter calls do), 32 rows a block.
+// rounded to bf16 (as the one-adapter calls do).  Four rows a block: lane 8 k +
+// j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
+// and the eight sums of a column meet by a butterfly, so that the loads of 56
+// ranges (K = 14336) are one round trip.
 __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
-  const int64_t t = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3);
-  const int j0 = (threadIdx.x & 7) * 8;
-  if (t >= a.T) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int k0 = lane >> 3, j0 = (lane & 7) * 8;
   const int id = row_id(a, t);
-  u32x4 out = u32x4{0, 0, 0, 0};
+  if (t >= a.T) return;
+  f32x4 s0 = f32x4{0, 0, 0, 0}, s1 = s0;
   if (id >= 0 && j0 < a.r) {  // the rank is a multiple of 8
-    f32x4 s0 = f32x4{0, 0, 0, 0}, s1 = s0;
     const float* u = a.upart + t * a.r + j0;
-    const float s = a.scales[id];
 #pragma unroll 8
-    for (int k = 0; k < a.kc; ++k) {
+    for (int k = k0; k < a.kc; k += 8) {
       const f32x4* p = reinterpret_cast<const f32x4*>(u + (int64_t)k * a.T * a.r);
       s0 += p[0];
       s1 += p[1];
     }
-    out = u32x4{pack_bf2(s * s0[0], s * s0[1]), pack_bf2(s * s0[2], s * s0[3]), pack_bf2(s * s1[0], s * s1[1]),
-                pack_bf2(s * s1[2], s * s1[3])};
+    const float s = a.scales[id];
+    s0 *= s;
+    s1 *= s;
   }
-  *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) = out;
+#pragma unroll
+  for (int d = 8; d < 64; d <<= 1)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s0[i] += __shfl_xor(s0[i], d);
+      s1[i] += __shfl_xor(s1[i], d);
+    }
+  if (k0 == 0)
+    *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) =
+        u32x4{pack_bf2(s0[0], s0[1]), pack_bf2(s0[2], s0[3]), pack_bf2(s1[0], s1[1]), pack_bf2(s1[2], s1[3])};
 }
 
 // ---------------------------------------------------------------------------
@@ -952,7 +976,7 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
     if (p.tiles) {
       {
         TraceScope ts("multi_u", st);
-        hipLaunchKernelGGL(multi_u_kernel, dim3((unsigned)cdiv(d->T, 32)), dim3(256), 0, st, a);
+        hipLaunchKernelGGL(multi_u_kernel, dim3((unsigned)cdiv(d->T, 4)), dim3(256), 0, st, a);
         LAUNCH(hipGetLastError());
       }
       GemmArgs g{};
