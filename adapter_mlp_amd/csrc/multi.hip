@@ -292,23 +292,29 @@ __global__ __launch_bounds__(256) void multi_shrink_few_kernel(const MultiArgs a
 }
 
 // X W, and where nshrink > 0 U beside it in the same launch, neither waiting
-// for the other: blocks 0 .. nshrink - 1 form U (first, since they are short).
+// for the other.
+// The nshrink blocks that form U come last: the others, which take longer, are
+// then spread evenly over the CUs (in front, the shrink left some CUs two of
+// them and others none: 46 against 38 us at 67 rows of 4096 x 14336).
 template <int MT>
 __global__ __launch_bounds__(256, BaseCfg<MT>::PER_CU) void multi_few_kernel(const MultiArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[BaseCfg<MT>::SMEM];
   static_assert(BaseCfg<MT>::SMEM >= 3 * 4 * 1024, "the shrink's exchange");
-  const int b = blockIdx.x;
-  if (b < a.nshrink) {
-    const int bx = b / (a.kc * a.nz), kz = b % (a.kc * a.nz);
-    switch ((a.r + 15) / 16) {
-      case 1: shrink_few_block<1>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
-      case 2: shrink_few_block<2>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
-      case 3: shrink_few_block<3>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
-      default: shrink_few_block<4>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
-    }
+  const int b = (int)blockIdx.x - ((int)gridDim.x - a.nshrink);
+  if (b < 0) {
+    base_block<MT>(a, lds, blockIdx.x);
     return;
   }
-  base_block<MT>(a, lds, b - a.nshrink);
+  const int bx = b / (a.kc * a.nz), kz = b % (a.kc * a.nz);
+  switch ((a.r + 15) / 16) {
+    case 1: shrink_few_block<1>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+    case 2: shrink_few_block<2>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+    case 3: shrink_few_block<3>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+    default: shrink_few_block<4>(a, lds, bx, kz / a.nz, kz % a.nz, a.nz); break;
+  }
+  // the compiler joins both ways before the other's loop, where loads that it holds pending from here
+  // would make it wait for all loads in every step
+  wait_vmcnt<0>();
 }
 
 // ---------------------------------------------------------------------------
@@ -758,19 +764,19 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
 // Which path a bf16 call takes.  Few rows: W is streamed through 128-column
 // tiles with K split over the grid, and the adapters join the fp32 sums as
 // those are added up.  Many: the 256 x 256 tiles of the GEMM, with the adapters
-// in its epilogue.  Fitted to both, timed from 130 to 1024 rows (rank 16 to 64;
-// us, few / many):
-//    4096 x 4096: 30 / 61 at 130 rows, 53 / 62 at 512, 72 / 64 at 640
-//    4096 x 14336: 44 / 67 at 130, 71 / 74 at 256, 101 / 85 at 300
-//    14336 x 4096: 54 / 103 at 130, 108 / 111 at 300, 120 / 107 at 384
-//    4096 x 1024: 57 / 55 at 1024;  640 x 640: 26 / 40 at 1024
-// few takes about T K N / 3e8 + T K / 1.9e5 + 16 us, many T K N / 1.1e9 +
-// K / 213 + 38 us; up to kFewRows rows always, and past 1024 never.
+// in its epilogue.  A rule fitted to both, timed from 130 to 1536 rows (us, few
+// / many):
+//    4096 x 4096: 24 / 57 at 130 rows, 53 / 57 at 512, 60 / 59 at 640
+//    4096 x 14336: 49 / 62 at 130, 64 / 72 at 256, 92 / 84 at 300
+//    14336 x 4096: 48 / 96 at 130, 87 / 99 at 256, 114 / 103 at 300
+//    4096 x 1024: 47 / 52 at 777, 57 / 50 at 1024;  640 x 640: 23 / 37 at 1024
+// few grows as T K N / 3e8 + T K / 1.9e5 us, many starts at 38 + K / 213; up to
+// kFewRows rows always, and past 1024 never.
 constexpr int64_t kFewRows = 128;
 bool few_rows(int64_t T, int64_t K, int64_t N) {
   if (T <= kFewRows || T > 1024) return T <= kFewRows;
   const double t = (double)T, k = (double)K;
-  return t * k * ((double)N / 4.1e8 + 1 / 1.9e5) < 0.85 * (22 + k / 213);
+  return t * k * ((double)N / 4.1e8 + 1 / 1.9e5) < 0.75 * (22 + k / 213);
 }
 
 // Row tiles of at most 128 rows, and the 16-row blocks of each.
@@ -785,27 +791,29 @@ int shrink_blocks(int64_t T, int64_t K, int64_t n) {
   return n == 0 ? 0 : (int)cdiv(T, 16) * shrink_ranges(true, K) * shrink_share(n);
 }
 
-// K ranges of X W for few rows, by a model of the grid: rounds of the blocks
-// that the chip holds, each as long as its K stages (16 KB of W at the CU's
-// share of HBM) and some 3 us to fill and drain, the fp32 parts that are
-// written and read again, and the shrink's 4 us where its blocks find no room
-// beside the others.
-int base_ksplit(int64_t T, int64_t K, int64_t N, int shrink) {
-  const int mt = row_blocks(T), per_cu = mt <= 5 ? 2 : 1;
+// K ranges of X W for few rows, by a model of what grows with them: the K
+// stages of the fullest CU, 0.3 to 0.6 us each with 16 to 128 rows, against the
+// fp32 parts, written and read again at some 3 TB/s.  (67 rows of 14336 x 4096:
+// 76 us with 2 ranges, 41 with 8, 47 with 16; 32 rows of 4096 x 4096: 33 us with
+// 1, 17 with 4, 21 with 16.)
+int base_ksplit(int64_t T, int64_t K, int64_t N) {
   const int64_t units = cdiv(N, 128) * row_tiles(T), steps = K / 64;
   double best = 0.0;
   int bs = 1;
   for (int s = 1; s <= 32 && (s == 1 || steps / s >= 4); ++s) {
-    const double rounds = (double)cdiv(units * s, 256 * per_cu);
-    const double t = rounds * ((double)cdiv(steps, s) * 0.8 * per_cu + 3.0) + (double)s * T * N * 8 / 4e6 +
-                     (units * s + shrink > 256 * per_cu ? 4.0 : 0.0);
-    if (s == 1 || t < best * 0.97) {
+    const double t = (0.3 + 0.04 * row_blocks(T)) * (double)(cdiv(units * s, 256) * cdiv(steps, s)) + (double)s * T * N * 8 / 3e6;
+    if (s == 1 || t < best * 0.98) {
       best = t;
       bs = s;
     }
   }
   return bs;
 }
+
+// The shrink joins the launch of X W up to this many blocks: it then starts at
+// once and fills what the others leave free, but takes their amount of LDS
+// (20 blocks to 1536: 2 to 12 us less joined; 2048 and more: 3 to 30 us more).
+constexpr int kJoin = 1536;
 
 hipError_t launch_shrink_few(const MultiArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)a.nshrink);
@@ -865,7 +873,7 @@ MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   p.few = base ? few_rows(d.T, d.K, d.N) : d.T <= kFewRows;
   p.tiles = bf16 && base && !p.few;
   p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K)
-                                              : base_ksplit(d.T, d.K, d.N, shrink_blocks(d.T, d.K, d.n));
+                                              : base_ksplit(d.T, d.K, d.N);
   p.kc = bf16 ? shrink_ranges(p.few, d.K) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
@@ -963,9 +971,7 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
       a.ntm = row_tiles(d->T);
       a.nz = shrink_share(d->n);
       a.nshrink = shrink_blocks(d->T, d->K, d->n);
-      // one launch saves a few us; but the shrink's blocks then take the LDS of the others, which
-      // many of them would wait for
-      if (d->T > kFewRows && a.nshrink > 0) {
+      if (a.nshrink > kJoin) {
         LAUNCHN("multi_shrink_few", st, launch_shrink_few(a, st));
         a.nshrink = 0;
       }
