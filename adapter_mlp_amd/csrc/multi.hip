@@ -21,8 +21,8 @@ struct MultiArgs {
   int64_t T, K, N, n;
   int32_t r, ks, kc, ntn, ntm;
   int32_t nshrink, nz;  // few rows: blocks of the shrink, and how many share the adapters of 16 rows
-  uint16_t* u;       // [T, 64] bf16: scaled U, zero past the rank (many rows)
-  MultiTile* plan;   // adapters of every 256-row tile (many rows)
+  uint16_t* u;          // [T, 64] bf16: scaled U, zero past the rank (many rows)
+  MultiTile* plan;      // adapters of every 256-row tile (many rows)
 };
 
 // The adapter of a row, -1 for none.
@@ -878,9 +878,7 @@ MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
   if (p.tiles) p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
-  if (bf16 && !p.few) {
-    p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
-  }
+  if (bf16 && !p.few) p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
   if (bf16 && base && (!p.tiles || p.ks > 1)) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
   p.bytes = w.off;
   return p;
@@ -894,6 +892,8 @@ lora_status check_multi(const lora_multi_desc* d) {
   const int64_t es = bf16 ? 2 : 4, lim = ((int64_t)1 << 31) - 4096;
   CHECK(d->T >= 0, LORA_ESHAPE, "T = %lld is negative", (long long)d->T);
   CHECK(d->K > 0 && d->N > 0, LORA_ESHAPE, "K = %lld and N = %lld must be positive", (long long)d->K, (long long)d->N);
+  CHECK(d->K <= (1 << 22) && d->N <= (1 << 22), LORA_ESHAPE, "K = %lld and N = %lld must be at most %d", (long long)d->K,
+        (long long)d->N, 1 << 22);
   CHECK(d->r >= 1 && d->r <= 64, LORA_ESHAPE, "rank r = %lld must be in [1, 64]", (long long)d->r);
   CHECK(d->n >= 0 && d->n < ((int64_t)1 << 31), LORA_ESHAPE, "n = %lld adapters", (long long)d->n);
   if (bf16) {
@@ -916,7 +916,8 @@ extern "C" {
 
 lora_status lora_multi_workspace_size(const lora_multi_desc* d, size_t* bytes) {
   TRY(check_multi(d));
-  if (bytes) *bytes = plan_multi(*d, true, nullptr).bytes;
+  // with W or without, the larger
+  if (bytes) *bytes = std::max(plan_multi(*d, true, nullptr).bytes, plan_multi(*d, false, nullptr).bytes);
   return LORA_OK;
 }
 

@@ -394,14 +394,15 @@ lora_status lora_o_bwd(const lora_o_desc* desc, const void* dY, const void* X, c
  * [T] names each row's.  LORA_BF16 or LORA_F32. */
 typedef struct lora_multi_desc {
   int64_t T;   /* rows of X: tokens of all requests */
-  int64_t K;   /* input width n_in */
-  int64_t N;   /* output width n_out */
+  int64_t K;   /* input width n_in, at most 2^22 */
+  int64_t N;   /* output width n_out, at most 2^22 */
   int64_t r;   /* rank of the adapters */
   int64_t n;   /* adapters in the stacks (0: none, A, B and scales may be NULL) */
   int32_t dtype;
   int32_t reserved; /* must be 0 */
 } lora_multi_desc;
 
+/* Enough for calls with and without W. */
 lora_status lora_multi_workspace_size(const lora_multi_desc* desc, size_t* bytes);
 
 /* Y[t] = X[t] W + scales[i] (X[t] A[i]) B[i], i = ids[t]; a row whose id lies

@@ -109,6 +109,17 @@ def test_added_to_a_base(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r", [(300, 14336, 64, 64), (129, 2048, 64, 8), (128, 2048, 64, 8), (1100, 320, 64, 40)])
+def test_one_workspace_for_both_forms(T, K, N, r):
+    """The size that is asked for covers the call without W too, whichever path the one with W takes."""
+    s = make(T, K, N, r, 5)
+    ws = torch.empty(lm.multi_workspace_size(T, K, N, r, 5), dtype=torch.uint8, device="cuda")
+    check(run(s, ws=ws), reference(s))
+    base = torch.zeros(T, N, dtype=torch.bfloat16, device="cuda")
+    check(lm.multi_fwd(s["X"], None, s["pool"], s["ids"], Y=base.clone(), ws=ws), reference(s, base))
+
+
+@pytest.mark.gpu
 def test_beside_an_nf4_base():
     s = make(40, 512, 512, 16, 5)
     q = lm.nf4_quantize(s["W"])
@@ -241,7 +252,7 @@ def test_library_refuses():
         return L.load().lora_multi_fwd(ctypes.byref(d), *at, nbytes, None)
 
     for kw, want in ((dict(T=-1), L.LORA_ESHAPE), (dict(K=96), L.LORA_ESHAPE), (dict(N=0), L.LORA_ESHAPE), (dict(r=12), L.LORA_ESHAPE),
-                     (dict(r=72), L.LORA_ESHAPE), (dict(r=0), L.LORA_ESHAPE), (dict(n=-1), L.LORA_ESHAPE), (dict(K=1 << 40), L.LORA_ESHAPE),
+                     (dict(r=72), L.LORA_ESHAPE), (dict(r=0), L.LORA_ESHAPE), (dict(n=-1), L.LORA_ESHAPE), (dict(K=1 << 40), L.LORA_ESHAPE), (dict(K=(1 << 22) + 64, N=64), L.LORA_ESHAPE),
                      (dict(T=1 << 40), L.LORA_ESHAPE), (dict(T=1 << 24), L.LORA_ESHAPE), (dict(dtype=L.LORA_BF16_F32LORA), L.LORA_EDTYPE),
                      (dict(rsv=3), L.LORA_EINVAL), (dict(X=0), L.LORA_EINVAL), (dict(A=0), L.LORA_EINVAL), (dict(B=0), L.LORA_EINVAL),
                      (dict(sc=0), L.LORA_EINVAL), (dict(ids=0), L.LORA_EINVAL), (dict(Y=0), L.LORA_EINVAL), (dict(off=8), L.LORA_EALIGN),
