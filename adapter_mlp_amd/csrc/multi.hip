@@ -59,6 +59,8 @@ __device__ __forceinline__ void wait_stages(int after) {
 // LDS layouts: W rows of 256 bytes, 16-byte chunk c of row k at c ^ 4 (k & 3),
 // read with the transposing LDS read; X rows of 128 bytes, chunk c of row m at
 // c ^ (m & 7).
+// Measured, U beside it: one row of 4096 x 4096 8.2 us (4.1 TB/s over W), 67
+// rows of 4096 x 14336 27 us (117 MB of W: 4.3 TB/s, a large copy 4.85).
 // ---------------------------------------------------------------------------
 template <int MT>
 struct BaseCfg {
@@ -328,6 +330,8 @@ __global__ __launch_bounds__(256, BaseCfg<MT>::PER_CU) void multi_few_kernel(con
 // block of a tile also lists its adapters for the GEMM.  (Blocks of 32 or 64
 // rows, each sorting the tile for itself, took longer to sort than to read X,
 // and A_i by loads into registers left each adapter a chain of latencies.)
+// Measured: 8192 rows of 4096 at rank 16, 67 MB of X: 23 us (2.9 TB/s); 777
+// rows of 14336 at rank 64 with 12 adapters: 26 us, the walk over the adapters.
 // ---------------------------------------------------------------------------
 // Rows of a 256-row tile in the order of their adapters (rows without one
 // last), by 256 threads: id_of and row_of hold the sorted ids and rows.
@@ -473,7 +477,7 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
 // rounded to bf16 (as the one-adapter calls do).  Four rows a block: lane 8 k +
 // j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
 // and the eight sums of a column meet by a butterfly, so that the loads of 56
-// ranges (K = 14336) are one round trip.
+// ranges (K = 14336) are one round trip.  6 us at both sizes above.
 __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
@@ -511,6 +515,8 @@ __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
 // wavefronts share the K parts and the ranks of all four rows, so that few
 // rows still have enough loads in flight, and meet in LDS, where wavefront w
 // adds them in ascending order for row w.
+// Measured: one row of 4096 5 us, 67 rows of 14336 at rank 16 8.7 us (7.7 MB of
+// parts, 14.7 MB of B_i): latency, with the launch that precedes it.
 // ---------------------------------------------------------------------------
 // Eight columns of a row.
 struct Cols {
@@ -535,6 +541,7 @@ struct Cols {
     }
   }
 };
+
 __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
   constexpr int C = 8;
   __shared__ float us[4][64];
@@ -644,6 +651,8 @@ __global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a
 //   tiles still fill the chip, and the chain of loads is a quarter as long.
 //   Else 64 x 64 a block, a quadrant a wavefront: half the traffic.
 // The adapter's term joins in the epilogue, from U of the tile's rows in LDS.
+// Measured: 128 rows of 256 x 704 9.2 us, behind 4.2 us for U: a chain of loads
+// and products too short to fill the chip, not the 0.9 MB that it moves.
 // ---------------------------------------------------------------------------
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 

@@ -129,6 +129,10 @@ constexpr bool norm_keep(bool bwd) {
 
 // Thread tx of a row's TPR threads owns the vectors tx, tx + TPR, ... (NV of
 // them) in every row it meets.
+// Measured: 8192 bf16 rows of 4096 with post-norm, column gate and pre-norm,
+// 268 MB: 46 us, 5.8 TB/s (a large copy: 4.85 TB/s, half of it written here as
+// there; operands that were just read or written partly come from the last-level
+// cache).  One row of 4096: 3 us, the round trips of its loads and one sum.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormArgs a) {
   constexpr bool PREFETCH = norm_prefetch<TA, VEC, TPR, NV>(false), KEEP = norm_keep<TA, VEC, TPR, NV>(false);
@@ -246,6 +250,9 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
 // need d).  The column sums of the parameter gradients gather in the
 // registers of the thread that owns the column, one slice per block, and
 // norm_grad_kernel adds the slices in ascending order.
+// Measured: 8192 bf16 rows of 4096 with all three gradients, 403 MB and 25 MB of
+// slices: 81 us, 5.3 TB/s, and 5.5 us to add the slices.  1003 fp32 rows of 1001
+// (no 16-byte access, a row of 1001 at odd addresses): 12.8 + 3.9 us.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(norm_block<TPR>(), TPR <= 256 ? 2 : 1) void norm_bwd_kernel(const NormArgs a) {
   constexpr bool PREFETCH = norm_prefetch<TA, VEC, TPR, NV>(true), KEEP = norm_keep<TA, VEC, TPR, NV>(true);

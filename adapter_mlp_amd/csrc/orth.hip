@@ -250,6 +250,10 @@ __device__ __forceinline__ const OrthGroup& my_group(const OrthArgs& a, int laun
 // four k to the lane groups gives the same sum) and short index NT c + t, and
 // serves as both sides of the product.  Only the tiles on and above the
 // diagonal are formed.  The wavefronts work alone until their sums meet.
+// Measured: momentum form over 448 rank-16 matrices, 503 MB: 95 us, 5.3 TB/s, the
+// bound there.  14 rank-64 matrices, 63 MB: 25 us; the matrix cores need 8 of
+// them (10 tiles a sub-tile of 16), the rest is a call too short to fill the
+// chip: one wave of blocks loads, multiplies, and joins its sums.
 template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const OrthArgs a) {
   constexpr int NP = NT * (NT + 1) / 2;
@@ -340,6 +344,10 @@ __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const O
 // wavefront, so that the four matrix cores share each product evenly and one
 // wavefront's LDS reads hide behind another's MFMAs.  Rows are 16 NT + 2
 // doubles apart, which spreads the 16 rows of a fragment read over all banks.
+// Measured: 5 steps 52 us at rank 64, 11 us at rank 16 (a single wavefront's
+// chain of products), whatever the number of matrices up to the chip's CUs.
+// fp32 products would halve that and lose the small singular values: an error
+// of 2^-24 |G| in a direction of G's null space grows by a^2 a step.
 template <int NT>
 __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, NP = NT * (NT + 1) / 2, THREADS = NT >= 3 ? 1024 : 256 * NT;
@@ -449,6 +457,9 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
 // A wavefront works alone on its sub-tile: U goes to LDS, 16 rows
 // (columns) at a time are multiplied and replaced there by O, which is then
 // read back as it lies in memory for the update of P (loaded with U).
+// Measured: the update of 448 rank-16 matrices, 671 MB: 130 us, 5.2 TB/s, the
+// bound.  14 rank-64 matrices, 84 MB: 35 us, of which the full products in fp64
+// (16 tiles a sub-tile) take 13.
 template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_apply_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, S = N / 4;
