@@ -477,8 +477,9 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
 // rounded to bf16 (as the one-adapter calls do).  Four rows a block: lane 8 k +
 // j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
 // and the eight sums of a column meet by a butterfly, so that the loads of 56
-// ranges (K = 14336) are one round trip.  6 us at both sizes above.
+// ranges (K = 14336) are two round trips.  5 to 7 us at both sizes above.
 __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
+  constexpr int AHEAD = 4;  // ranges a lane loads together (past the last one it is read again)
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   const int k0 = lane >> 3, j0 = (lane & 7) * 8;
@@ -487,11 +488,19 @@ __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
   f32x4 s0 = f32x4{0, 0, 0, 0}, s1 = s0;
   if (id >= 0 && j0 < a.r) {  // the rank is a multiple of 8
     const float* u = a.upart + t * a.r + j0;
-#pragma unroll 8
-    for (int k = k0; k < a.kc; k += 8) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(u + (int64_t)k * a.T * a.r);
-      s0 += p[0];
-      s1 += p[1];
+    for (int k = k0; k < a.kc; k += 8 * AHEAD) {
+      f32x4 x[AHEAD][2];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(u + (int64_t)min(k + 8 * i, a.kc - 1) * a.T * a.r);
+        x[i][0] = p[0];
+        x[i][1] = p[1];
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        s0 = k + 8 * i < a.kc ? s0 + x[i][0] : s0;
+        s1 = k + 8 * i < a.kc ? s1 + x[i][1] : s1;
+      }
     }
     const float s = a.scales[id];
     s0 *= s;
@@ -623,17 +632,32 @@ __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
 }
 
 // U in fp32: one block per row; threads are (K slot, rank index), slots added in ascending order.
-__global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a) {
-  __shared__ float red[256];
+// A thread's chain of round trips is the bound, so a rank above 16 gets 1024
+// threads (65 rows of 1500 at rank 64: 14 us, 28 with 256) and a lower one,
+// whose slots are many already, 256 (128 rows of 256 at rank 8: 3.7 us).
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void multi_shrink_f32_kernel(const MultiArgs a) {
+  constexpr int AHEAD = THREADS > 256 ? 16 : 8;  // K a thread loads together (past the last one it is read again)
+  __shared__ float red[THREADS];
   const int64_t t = blockIdx.x;
   const int id = row_id(a, t);
   if (id < 0) return;  // uniform
-  const int slots = 256 / a.r, slot = threadIdx.x / a.r, j = threadIdx.x % a.r;
+  const int slots = THREADS / a.r, slot = threadIdx.x / a.r, j = threadIdx.x % a.r;
   const float* x = static_cast<const float*>(a.X) + t * a.K;
   const float* A = static_cast<const float*>(a.A) + (int64_t)id * a.K * a.r;
   float s = 0.0f;
   if (slot < slots)
-    for (int64_t k = slot; k < a.K; k += slots) s = fmaf(x[k], A[k * a.r + j], s);
+    for (int64_t k0 = slot; k0 < a.K; k0 += AHEAD * slots) {
+      float xs[AHEAD], as[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int64_t k = min(k0 + i * slots, a.K - 1);
+        xs[i] = x[k];
+        as[i] = A[k * a.r + j];
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) s = k0 + i * slots < a.K ? fmaf(xs[i], as[i], s) : s;
+    }
   red[threadIdx.x] = s;
   __syncthreads();
   if (slot == 0) {
@@ -651,14 +675,16 @@ __global__ __launch_bounds__(256) void multi_shrink_f32_kernel(const MultiArgs a
 //   tiles still fill the chip, and the chain of loads is a quarter as long.
 //   Else 64 x 64 a block, a quadrant a wavefront: half the traffic.
 // The adapter's term joins in the epilogue, from U of the tile's rows in LDS.
-// Measured: 128 rows of 256 x 704 9.2 us, behind 4.2 us for U: a chain of loads
-// and products too short to fill the chip, not the 0.9 MB that it moves.
+// Measured: 128 rows of 256 x 704 7.2 us: a chain of loads and products too short
+// to fill the chip, not the 0.9 MB that it moves.  4096 rows of 1024 x 1024 138
+// us, 62 TFLOP/s of the 152 a library product reaches: no operand is shared
+// through LDS.
 // ---------------------------------------------------------------------------
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 template <bool KSPLIT>
 __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
-  constexpr int TILE = KSPLIT ? 32 : 64;
+  constexpr int TILE = KSPLIT ? 32 : 64, DEPTH = 4;  // DEPTH steps of loads in flight
   __shared__ f32x4 red[KSPLIT ? 4 : 1][KSPLIT ? 4 : 1][64];
   __shared__ float us[TILE][65];
   __shared__ int ids[TILE];
@@ -684,38 +710,61 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
     const int64_t k0 = KSPLIT ? w * quarter : 0;
     const int64_t k1 = KSPLIT && k0 + quarter < a.K ? k0 + quarter : a.K;
     const float *X = static_cast<const float*>(a.X), *W = static_cast<const float*>(a.W);
-    float x[2][2][4], wv[2][2][4];  // [buffer][tile][k]
-    auto load = [&](int64_t k, float (&xo)[2][4], float (&wo)[2][4]) {
-      const int64_t kk = k + 4 * g;
+    // Rows and columns past the end read the last one, whose sums are not stored: no load is guarded.
+    const float *xr[2], *wc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      xr[i] = X + min(m0 + 16 * i + c, a.T - 1) * a.K + 4 * g;
+      wc[i] = W + min(n0 + 16 * i + c, a.N - 1) + 4 * g * a.N;
+    }
+    f32x4 x[DEPTH][2];
+    float wv[DEPTH][2][4];
+    auto load = [&](int s, int64_t k) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int64_t m = m0 + 16 * i + c, n = n0 + 16 * i + c;
-        if (m < a.T && kk + 4 <= k1) {
-          const f32x4u v = *reinterpret_cast<const f32x4u*>(X + m * a.K + kk);
+        x[s][i] = *reinterpret_cast<const f32x4u*>(xr[i] + k);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) xo[i][q] = v[q];
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) xo[i][q] = m < a.T && kk + q < k1 ? X[m * a.K + kk + q] : 0.0f;
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) wo[i][q] = n < a.N && kk + q < k1 ? W[(kk + q) * a.N + n] : 0.0f;
+        for (int q = 0; q < 4; ++q) wv[s][i][q] = wc[i][(k + q) * a.N];
       }
     };
-    auto mma = [&](const float (&xi)[2][4], const float (&wi)[2][4]) {
+    auto mma = [&](int s) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xi[i][q], wi[j][q], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < 2; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(x[s][i][q], wv[s][j][q], acc[i][j], 0, 0, 0);
     };
-    if (k0 < k1) load(k0, x[0], wv[0]);
-    for (int64_t k = k0; k < k1; k += 32) {
-      if (k + 16 < k1) load(k + 16, x[1], wv[1]);
-      mma(x[0], wv[0]);
-      if (k + 32 < k1) load(k + 32, x[0], wv[0]);
-      if (k + 16 < k1) mma(x[1], wv[1]);
+    int64_t k = k0;
+    if (k0 + 16 * DEPTH <= k1) {
+#pragma unroll
+      for (int s = 0; s < DEPTH; ++s) load(s, k0 + 16 * s);
+      for (; k + 32 * DEPTH <= k1; k += 16 * DEPTH)
+#pragma unroll
+        for (int s = 0; s < DEPTH; ++s) {
+          mma(s);
+          load(s, k + 16 * (DEPTH + s));
+        }
+#pragma unroll
+      for (int s = 0; s < DEPTH; ++s) mma(s);
+      k += 16 * DEPTH;
+    }
+    for (; k + 16 <= k1; k += 16) {
+      load(0, k);
+      mma(0);
+    }
+    if (k < k1) {  // fewer than 16 K: zeros past them on both sides
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t kk = k + 4 * g + q, kc = min(kk, a.K - 1) - 4 * g;
+          const float xv = xr[i][kc], v = wc[i][kc * a.N];
+          x[0][i][q] = kk < k1 ? xv : 0.0f;
+          wv[0][i][q] = kk < k1 ? v : 0.0f;
+        }
+      mma(0);
     }
   }
   if constexpr (KSPLIT) {
@@ -736,22 +785,33 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
       id[v] = ids[row + v];
       if (a.W == nullptr && mt + row + v < a.T) y[v] = static_cast<const float*>(a.Y)[(mt + row + v) * a.N + n];
     }
-    const float* B = static_cast<const float*>(a.B);
+    const float* B = static_cast<const float*>(a.B) + n;
     const int64_t bs = (int64_t)a.r * a.N;
     if (id[0] == id[1] && id[0] == id[2] && id[0] == id[3]) {
       if (id[0] >= 0)
-#pragma unroll 4
-        for (int k = 0; k < a.r; ++k) {
-          const float b = B[id[0] * bs + (int64_t)k * a.N + n];
+        for (int k0 = 0; k0 < a.r; k0 += 8) {
+          float b[8];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) y[v] = fmaf(us[row + v][k], b, y[v]);
+          for (int k = 0; k < 8; ++k) b[k] = B[id[0] * bs + (int64_t)min(k0 + k, a.r - 1) * a.N];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] = k0 + k < a.r ? fmaf(us[row + v][min(k0 + k, a.r - 1)], b[k], y[v]) : y[v];
         }
-    } else {
+    } else {  // at least one of the four has an adapter: a row without one reads that one's ranks
+      const int top = max(max(id[0], id[1]), max(id[2], id[3]));
+      for (int k0 = 0; k0 < a.r; k0 += 8) {
+        float b[4][8];
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        if (id[v] >= 0)
-#pragma unroll 4
-          for (int k = 0; k < a.r; ++k) y[v] = fmaf(us[row + v][k], B[id[v] * bs + (int64_t)k * a.N + n], y[v]);
+        for (int v = 0; v < 4; ++v)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) b[v][k] = B[(id[v] < 0 ? top : id[v]) * bs + (int64_t)min(k0 + k, a.r - 1) * a.N];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            y[v] = id[v] >= 0 && k0 + k < a.r ? fmaf(us[row + v][min(k0 + k, a.r - 1)], b[v][k], y[v]) : y[v];
+      }
     }
 #pragma unroll
     for (int v = 0; v < 4; ++v)
@@ -1030,7 +1090,8 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   }
   if (d->n > 0) {
     TraceScope ts("multi_shrink_f32", st);
-    hipLaunchKernelGGL(multi_shrink_f32_kernel, dim3((unsigned)d->T), dim3(256), 0, st, a);
+    if (d->r > 16) hipLaunchKernelGGL(multi_shrink_f32_kernel<1024>, dim3((unsigned)d->T), dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL(multi_shrink_f32_kernel<256>, dim3((unsigned)d->T), dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
   } else if (W == nullptr) {
     return LORA_OK;

@@ -439,13 +439,19 @@ struct NormGradArgs {
 };
 template <typename TP>
 __global__ __launch_bounds__(1024) void norm_grad_kernel(const NormGradArgs a) {
+  constexpr int AHEAD = 16;  // slices a thread loads together (past the last one it is read again)
   __shared__ float run[16][64];
   const int c = blockIdx.x * 64 + (threadIdx.x & 63), k = threadIdx.x >> 6;
   const float* p = a.part[blockIdx.y];
   float s = 0.0f;
   if (c < a.H)
-#pragma unroll 8
-    for (int b = k; b < a.nb; b += 16) s += p[(int64_t)b * a.H + c];
+    for (int b0 = k; b0 < a.nb; b0 += 16 * AHEAD) {
+      float x[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) x[i] = p[(int64_t)min(b0 + 16 * i, a.nb - 1) * a.H + c];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) s = b0 + 16 * i < a.nb ? s + x[i] : s;
+    }
   run[k][threadIdx.x & 63] = s;
   __syncthreads();
   if (k == 0 && c < a.H) {

@@ -344,9 +344,11 @@ __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const O
 // wavefront, so that the four matrix cores share each product evenly and one
 // wavefront's LDS reads hide behind another's MFMAs.  Rows are 16 NT + 2
 // doubles apart, which spreads the 16 rows of a fragment read over all banks.
-// Measured: 5 steps 52 us at rank 64, 11 us at rank 16 (a single wavefront's
-// chain of products), whatever the number of matrices up to the chip's CUs.
-// fp32 products would halve that and lose the small singular values: an error
+// Measured: 5 steps 46 to 52 us at rank 64 (6.5 a step, 4.7 of it the matrix
+// cores; the rest is the chunks' sum, 20 KB each into one CU, and the way in and
+// out), 9 us at rank 16 (0.9 a step, a chain of products), whatever the number
+// of matrices up to the chip's CUs.
+// fp32 products would halve the steps and lose the small singular values: an error
 // of 2^-24 |G| in a direction of G's null space grows by a^2 a step.
 template <int NT>
 __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(const OrthArgs a) {
@@ -360,17 +362,34 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
   const int q = lane >> 4, c = lane & 15;
 
   // sum of the chunks, ascending; element (i, v, lane) is row 16 t + 4 v + q, column 16 s + c
+  // (every thread's elements of AHEAD chunks are loaded together; past the last chunk it is read again)
   const double* part = g.part + (int64_t)mat * g.chunks * (NP * 256);
-  for (int e = threadIdx.x; e < NP * 256; e += THREADS) {
-    double s = 0.0;
-#pragma unroll 16
-    for (int k = 0; k < g.chunks; ++k) s += part[(int64_t)k * (NP * 256) + e];
+  constexpr int PER = (NP * 256 + THREADS - 1) / THREADS, AHEAD = PER > 2 ? 12 : 16;
+  double sum[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) sum[j] = 0.0;
+  for (int k0 = 0; k0 < g.chunks; k0 += AHEAD) {
+    double x[AHEAD][PER];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        x[k][j] = part[(int64_t)min(k0 + k, g.chunks - 1) * (NP * 256) + min((int)threadIdx.x + j * THREADS, NP * 256 - 1)];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int j = 0; j < PER; ++j) sum[j] = k0 + k < g.chunks ? sum[j] + x[k][j] : sum[j];
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int e = threadIdx.x + j * THREADS;
+    if (e >= NP * 256) break;
     const int i = e >> 8, v = (e >> 6) & 3, l = e & 63;
     int t = 0, first = 0;
     while (i >= first + NT - t) first += NT - t++;
     const int row = 16 * t + 4 * v + (l >> 4), col = 16 * (t + i - first) + (l & 15);
-    mg[row * LD + col] = s;
-    if (i != first) mg[col * LD + row] = s;
+    mg[row * LD + col] = sum[j];
+    if (i != first) mg[col * LD + row] = sum[j];
   }
   __syncthreads();
   double trace = lane < N ? mg[lane * LD + lane] : 0.0;

@@ -6,7 +6,11 @@
  * transformer block: the gated LoRA MLP (gate, up and down projections around
  * a SwiGLU or GeGLU activation), the LoRA Q/K/V projections and the single
  * LoRA projection used for the attention output (O), forward and backward,
- * with an optional NF4-packed frozen base weight.
+ * with an optional NF4-packed frozen base weight.  Around it: the adapters of
+ * many requests beside one shared projection (lora_multi_fwd), the norms
+ * before and after a block with its gate and residual (lora_block_norm_*),
+ * and orthogonalised updates of the adapters (lora_orthogonalize,
+ * lora_muon_step); these state their own shapes and types below.
  *
  * Sources the operations follow (cited by page title and section):
  *   [LO]  "LoRA Optimizations" -- Axolotl documentation: sections "Custom
@@ -38,7 +42,8 @@
  * dtype.  One compute dtype per call: LORA_BF16 (bf16 in and out, fp32
  *   accumulation) or LORA_F32 (fp32 throughout).  Every dense tensor of the
  *   call (X, W, A, B, outputs, saved tensors) has that dtype.  NF4 bases need
- *   bf16 compute (LORA_BF16 or LORA_BF16_F32LORA).
+ *   bf16 compute (LORA_BF16 or LORA_BF16_F32LORA).  Scales, momenta and row ids
+ *   have the types their calls state.
  *   LORA_BF16_F32LORA is the fp32 LoRA-gradient mode ([LO] "FP32 LoRA
  *   gradients"): the adapters A, B and the gradients dA, dB are fp32; every
  *   other tensor (X, W, dY, outputs, saved e, g, U, dX) is bf16.  Each call
@@ -63,7 +68,8 @@
  * Shapes (fp32).  Any positive widths, 1 <= r <= 64; 4-byte aligned pointers.
  * Extent (all dtypes).  The kernels address each operand with 32-bit byte
  *   offsets: every activation [T, width] and every weight must be smaller
- *   than 2 GiB - 4 KiB, else the call returns LORA_ESHAPE.
+ *   than 2 GiB - 4 KiB, else the call returns LORA_ESHAPE.  (lora_multi_fwd
+ *   holds to it; the norm and orthogonalisation calls take larger tensors.)
  * No dropout and no bias on the adapters ([LO] "Requirements").
  */
 #ifndef LORA_MI355X_H
