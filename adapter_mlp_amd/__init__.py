@@ -8,6 +8,14 @@ library's HIP kernels.
 Layouts follow the C header: W [n_in, n_out], A [n_in, r], B [r, n_out],
 row-major; bf16 or fp32 compute; NF4 bases in bf16.  bf16 inputs with fp32
 adapters select the fp32 LoRA-gradient mode (fp32 dA, dB).
+
+Beside the projections: ``multi_fwd`` (rows of one batch with different
+adapters), ``block_norm_fwd`` / ``block_norm_bwd`` (norms before and after a
+block with its gate and residual) and ``orthogonalize`` / ``muon_step``
+(orthogonalised updates of the adapters).  These run on the device of their
+tensors, current or not, on ``stream`` or that device's current stream, and
+can be captured into a graph; a workspace given as ``ws`` must not be in use
+by another call at the same time.
 """
 from __future__ import annotations
 
