@@ -395,7 +395,8 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
   double trace = lane < N ? mg[lane * LD + lane] : 0.0;
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
-  const double inv = 1.0 / (sqrt(trace) + a.eps);
+  const double norm = sqrt(trace) + a.eps;
+  const double inv = norm == 0.0 ? 0.0 : 1.0 / norm;  // zeros stay zeros whatever eps is
   __syncthreads();
   for (int e = threadIdx.x; e < N * N; e += THREADS) mg[e / N * LD + e % N] *= inv * inv;
   __syncthreads();

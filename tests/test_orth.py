@@ -115,6 +115,16 @@ def test_zero_deficient_extreme_and_bad_matrices():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("r", [4, 20, 40, 64])
+def test_zeros_without_eps(r):
+    G = rnd((2, 300, r))
+    G[0] = 0
+    out = lm.orthogonalize(G, eps=0.0)
+    assert not out[0].any()
+    check("rest", out[1:], ns64(G[1:], eps=0.0))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("shape", [(3, 900, 24), (3, 24, 900)])
 def test_in_place_other_stream_same_answer(shape):
     G = rnd(shape, torch.bfloat16)
