@@ -631,7 +631,7 @@ __global__ __launch_bounds__(256) void multi_expand_kernel(const MultiArgs a) {
   }
 }
 
-// U in fp32: one block per row; threads are (K slot, rank index), slots added in ascending order.
+// U in fp32: one block per row (x, then y); threads are (K slot, rank index), slots added in ascending order.
 // A thread's chain of round trips is the bound, so a rank above 16 gets 1024
 // threads (65 rows of 1500 at rank 64: 14 us, 28 with 256) and a lower one,
 // whose slots are many already, 256 (128 rows of 256 at rank 8: 3.7 us).
@@ -639,7 +639,7 @@ template <int THREADS>
 __global__ __launch_bounds__(THREADS) void multi_shrink_f32_kernel(const MultiArgs a) {
   constexpr int AHEAD = THREADS > 256 ? 16 : 8;  // K a thread loads together (past the last one it is read again)
   __shared__ float red[THREADS];
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   const int id = row_id(a, t);
   if (id < 0) return;  // uniform
   const int slots = THREADS / a.r, slot = threadIdx.x / a.r, j = threadIdx.x % a.r;
@@ -1090,8 +1090,11 @@ lora_status lora_multi_fwd(const lora_multi_desc* d, const void* X, const void* 
   }
   if (d->n > 0) {
     TraceScope ts("multi_shrink_f32", st);
-    if (d->r > 16) hipLaunchKernelGGL(multi_shrink_f32_kernel<1024>, dim3((unsigned)d->T), dim3(1024), 0, st, a);
-    else hipLaunchKernelGGL(multi_shrink_f32_kernel<256>, dim3((unsigned)d->T), dim3(256), 0, st, a);
+    // a launch may have 2^32 - 1 threads along x
+    const int64_t gx = std::min<int64_t>(d->T, 1 << 20);
+    const dim3 rows((unsigned)gx, (unsigned)cdiv(d->T, gx));
+    if (d->r > 16) hipLaunchKernelGGL(multi_shrink_f32_kernel<1024>, rows, dim3(1024), 0, st, a);
+    else hipLaunchKernelGGL(multi_shrink_f32_kernel<256>, rows, dim3(256), 0, st, a);
     LAUNCH(hipGetLastError());
   } else if (W == nullptr) {
     return LORA_OK;

@@ -211,6 +211,21 @@ def test_stacks_past_two_gib(T):
     assert torch.equal(got, run(s))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,N,r", [(8, 5, 33), (5, 8, 3)])
+def test_more_rows_than_a_grid_row(K, N, r):
+    T = (1 << 22) + 77 if r > 16 else (1 << 24) + 77
+    s = make(1000, K, N, r, 3, "f32")
+    reps = -(-T // 1000)
+    X = s["X"].repeat(reps, 1)[:T].contiguous()
+    ids = s["ids"].repeat(reps)[:T].contiguous()
+    got = lm.multi_fwd(X, s["W"], s["pool"], ids)
+    want = run(s)
+    full = T // 1000 * 1000
+    assert torch.equal(got[:full].view(-1, 1000, N), want.expand(full // 1000, 1000, N))
+    assert torch.equal(got[full:], want[:T - full])
+
+
 # ---- refusals (no GPU) ----
 
 def test_binding_refuses():
