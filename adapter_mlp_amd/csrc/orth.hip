@@ -41,6 +41,9 @@ constexpr int kMaxGroups = 24;  // stacks per launch (their table is a kernel ar
 constexpr int kSub = 2048;      // elements of U that a wavefront takes at a time, at most
 constexpr int kVecs = kSub / 256;    // 4-element vectors per lane of them
 constexpr int kRegion = 2560 + 64;   // floats of LDS a wavefront holds them in
+// A launch has fewer than 2^32 threads: blocks of 256, and of up to 1024 for the steps.  A stack of fewer
+// than 2^30 long-side elements in all has fewer blocks than that (a sub-tile has at least 32 of them).
+constexpr int64_t kMaxBlocks = (1 << 24) - 1, kMaxMats = (1 << 22) - 1, kMaxLong = 1 << 30;
 
 // One stack of `count` matrices with the same shape.
 struct OrthGroup {
@@ -669,7 +672,7 @@ lora_status check_orth(const lora_orth_desc* d, const lora_orth_mat* mats) {
     CHECK(m.rows <= 64 || m.cols <= 64, LORA_ESHAPE, "mats[%d]: neither side of [%lld, %lld] is at most 64", i,
           (long long)m.rows, (long long)m.cols);
     const Shape s = shape_of(m, 1);
-    CHECK(s.n < ((int64_t)1 << 30) && m.count <= ((int64_t)1 << 30) / s.chunks, LORA_ESHAPE,
+    CHECK(m.count < kMaxMats && s.n < kMaxLong && m.count < kMaxLong / s.n, LORA_ESHAPE,
           "mats[%d]: %lld x [%lld, %lld] is too large", i, (long long)m.count, (long long)m.rows, (long long)m.cols);
     CHECK(m.reserved == 0, LORA_EINVAL, "mats[%d].reserved must be 0", i);
   }
@@ -758,7 +761,8 @@ lora_status run_orth(const lora_orth_desc* d, const lora_orth_mat* mats, int mod
       double* part = static_cast<double*>(w.take(s.part));
       double* Q = static_cast<double*>(w.take(s.q));
       if (s.nt != nt || m.count == 0) continue;
-      if (a.ngroups == kMaxGroups || blocks[APPLY] + add[APPLY] > ((int64_t)1 << 30)) LAUNCH(flush());
+      if (a.ngroups == kMaxGroups || blocks[APPLY] + add[APPLY] > kMaxBlocks || blocks[STEPS] + add[STEPS] > kMaxMats)
+        LAUNCH(flush());
       for (int k = 0; k < 3; ++k) {
         a.first[k][a.ngroups] = (int32_t)blocks[k];
         blocks[k] += add[k];

@@ -490,7 +490,9 @@ lora_status lora_block_norm_bwd(const lora_norm_desc* desc, const void* dR_out, 
 
 /* A stack of `count` dense matrices [rows, cols], one side at most 64: the
  * adapters A [n_in, r] or B [r, n_out] of several layers or users.  G and P
- * have the descriptor's dtype (LORA_F32 or LORA_BF16), aligned to it. */
+ * have the descriptor's dtype (LORA_F32 or LORA_BF16), aligned to it.  A stack
+ * holds fewer than 2^22 - 1 matrices, and fewer than 2^30 rows of the short
+ * side's width in all; tensors may exceed 2 GiB. */
 typedef struct lora_orth_mat {
   const void* G;   /* gradient (read) */
   float* M;        /* lora_muon_step: momentum, fp32 (updated); else NULL */
@@ -522,14 +524,14 @@ lora_status lora_orth_workspace_size(const lora_orth_desc* desc, const lora_orth
  *   X_0 = G / (|G| + eps)   (Frobenius norm)
  *   X <- a X + (b S + c S S) X,  S = X X^T,   `steps` times
  * (for a tall G with the products on its other side).  Formed in fp64, rounded
- * once.  A matrix of zeros gives zeros.  P may be G itself; any other overlap
+ * to fp32 and then to the type.  A matrix of zeros gives zeros.  P may be G itself; any other overlap
  * returns LORA_EUNSUPPORTED. */
 lora_status lora_orthogonalize(const lora_orth_desc* desc, const lora_orth_mat* mats, void* ws, size_t ws_bytes,
                                void* stream);
 
 /* One optimizer step of every stack:
  *   M <- momentum M + G;  U = G + momentum M (nesterov) or M   (fp32)
- *   P <- (1 - lr weight_decay) P - lr scale NS(U)              (rounded once)
+ *   P <- (1 - lr weight_decay) P - lr scale NS(U)   (from the fp32 NS(U) in fp64)
  * No tensor may overlap another (LORA_EUNSUPPORTED). */
 lora_status lora_muon_step(const lora_muon_desc* desc, const lora_orth_mat* mats, void* ws, size_t ws_bytes,
                            void* stream);

@@ -181,6 +181,14 @@ def test_past_32_bit_offsets():
 
 
 @pytest.mark.gpu
+def test_many_small_matrices():
+    """More matrices than one launch of the steps takes."""
+    G = [rnd((1000, 20, 1), torch.bfloat16, seed=k).repeat(3000, 1, 1) for k in range(2)]
+    for got, want in zip(lm.orthogonalize(G), [lm.orthogonalize(g[:1000]) for g in G]):
+        assert torch.equal(got.view(3000, 1000, 20, 1), want.expand(3000, 1000, 20, 1))
+
+
+@pytest.mark.gpu
 def test_nothing_to_do():
     assert lm.orthogonalize([]) == []
     lm.muon_step([], [], [], lr=0.1)
@@ -236,6 +244,9 @@ def test_library_refuses():
                      (dict(mats=((1, 2, 0, -1, 100, 8, 1.0, 0),)), L.LORA_ESHAPE),
                      (dict(mats=((1, 2, 0, 1 << 40, 100, 8, 1.0, 0),)), L.LORA_ESHAPE),
                      (dict(mats=((1, 2, 0, 1, 1 << 40, 8, 1.0, 0),)), L.LORA_ESHAPE),
+                     (dict(mats=((1, 2, 0, (1 << 22) - 1, 33, 33, 1.0, 0),)), L.LORA_ESHAPE),
+                     (dict(mats=((1, 2, 0, 1 << 15, 1 << 15, 1, 1.0, 0),)), L.LORA_ESHAPE),
+                     (dict(mats=((1, 2, 0, 1, 1, 1 << 30, 1.0, 0),)), L.LORA_ESHAPE),
                      (dict(mats=((1, 2, 0, 1, 100, 8, 1.0, 1),)), L.LORA_EINVAL), (dict(mats=((0, 2, 0, 1, 100, 8, 1.0, 0),)), L.LORA_EINVAL),
                      (dict(mats=((1, 0, 0, 1, 100, 8, 1.0, 0),)), L.LORA_EINVAL), (dict(mats=((1, 2, 3, 1, 100, 8, 1.0, 0),)), L.LORA_EINVAL),
                      (dict(ws=None), L.LORA_EWORKSPACE), (dict(nbytes=1024), L.LORA_EWORKSPACE), (dict(ws=(1 << 30) + 8), L.LORA_EALIGN),
