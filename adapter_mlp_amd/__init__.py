@@ -619,11 +619,18 @@ def _call_on(t, stream, name, *args):
         raise ValueError(f"stream is on {stream.device}, expected {dev}")
     else:
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:  # torch.cuda.current_device() of an initialised process
         L.call(name, *args, raw)
     else:
         with torch.cuda.device(dev):
             L.call(name, *args, raw)
+
+
+def _work(ws, need, dev):
+    """The workspace of a call and its size: the caller's (as _on_gpu has checked it) or a new one."""
+    if ws is not None:
+        return ws, ws.numel() * ws.element_size()
+    return _torch().empty(need or 1, dtype=_torch().uint8, device=dev), need
 
 
 @dataclass
@@ -651,31 +658,31 @@ def multi_fwd(X, W, pool: AdapterPool, ids, *, Y=None, ws=None, stream=None):
     form (``nf4_gemm``).  Returns Y."""
     torch = _torch()
     T, K = _x2d("X", X)
-    if pool.A.dim() != 3 or pool.B.dim() != 3:
+    A, B, dtype, dev = pool.A, pool.B, X.dtype, X.device
+    if A.dim() != 3 or B.dim() != 3:
         raise ValueError("pool.A must be [n, n_in, r] and pool.B [n, r, n_out]")
-    n, _, r = pool.A.shape
-    N = pool.B.shape[2]
+    n, _, r = A.shape
+    N = B.shape[2]
     dt = _dtype_code(X)
-    _need("X", X, (T, K), X.dtype, X.device)
+    _need("X", X, (T, K), dtype, dev)
     if W is not None:
-        _need("W", W, (K, N), X.dtype, X.device)
-    _need("pool.A", pool.A, (n, K, r), X.dtype, X.device)
-    _need("pool.B", pool.B, (n, r, N), X.dtype, X.device)
-    _need("pool.scale", pool.scale, (n,), torch.float32, X.device)
-    _need("ids", ids, (T,), torch.int32, X.device)
+        _need("W", W, (K, N), dtype, dev)
+    _need("pool.A", A, (n, K, r), dtype, dev)
+    _need("pool.B", B, (n, r, N), dtype, dev)
+    _need("pool.scale", pool.scale, (n,), torch.float32, dev)
+    _need("ids", ids, (T,), torch.int32, dev)
     if Y is not None:
-        _need("Y", Y, (T, N), X.dtype, X.device)
+        _need("Y", Y, (T, N), dtype, dev)
     elif W is None:
         raise ValueError("without W the adapter terms are added to Y, which is missing")
     _on_gpu(X, ws)
     d = L.lora_multi_desc(T, K, N, r, n, dt, 0)
     with _on(stream):
         if Y is None:
-            Y = torch.empty((T, N), dtype=X.dtype, device=X.device)
-        if ws is None:
-            ws = _ws(multi_workspace_size(T, K, N, r, n, dt), X.device)
-    _call_on(X, stream, "lora_multi_fwd", C.byref(d), _ptr(X), _ptr(W), _ptr(pool.A), _ptr(pool.B), _ptr(pool.scale),
-             _ptr(ids), _ptr(Y), _ptr(ws), _nbytes(ws, X.device))
+            Y = torch.empty((T, N), dtype=X.dtype, device=dev)
+        ws, ws_bytes = _work(ws, multi_workspace_size(T, K, N, r, n, dt), dev)
+    _call_on(X, stream, "lora_multi_fwd", C.byref(d), X.data_ptr(), _ptr(W), A.data_ptr(), B.data_ptr(),
+             pool.scale.data_ptr(), ids.data_ptr(), Y.data_ptr(), ws.data_ptr(), ws_bytes)
     return Y
 
 
@@ -685,30 +692,38 @@ def multi_fwd(X, W, pool: AdapterPool, ids, *, Y=None, ws=None, stream=None):
 
 def _norm_call(R, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset):
     """The checked descriptor of a block norm over rows like R's."""
-    torch = _torch()
     T, H = _x2d("R", R)
-    dt = _dtype_code(R)
-    _need("R", R, (T, H), R.dtype, R.device)
+    dt, shape, dtype, dev = _dtype_code(R), R.shape, R.dtype, R.device
+    _need("R", R, shape, dtype, dev)
     if Y is not None:
-        _need("Y", Y, (T, H), R.dtype, R.device)
-    kind = L.LORA_GATE_NONE
+        _need("Y", Y, shape, dtype, dev)
+    kind, col = L.LORA_GATE_NONE, None
     if gate is not None:
-        shape = tuple(gate.shape)
-        kind = (L.LORA_GATE_COL if shape == (H,) else L.LORA_GATE_ROW if shape == (T, 1)
-                else L.LORA_GATE_ELEM if shape == (T, H) else None)
-        if kind is None:
-            raise ValueError(f"gate has shape {shape}, expected ({H},), ({T}, 1) or ({T}, {H})")
-    params = [(n, p) for n, p in (("w_pre", w_pre), ("w_post", w_post), ("gate", gate if kind == L.LORA_GATE_COL else None))
-              if p is not None]
-    pd = params[0][1].dtype if params else R.dtype
-    if pd != R.dtype:
-        if R.dtype != torch.bfloat16 or pd != torch.float32:
-            raise ValueError(f"parameters in {pd} with activations in {R.dtype} are not supported")
-        dt = L.LORA_BF16_F32LORA
-    for n, p in params:
-        _need(n, p, (H,), pd, R.device)
-    if kind in (L.LORA_GATE_ROW, L.LORA_GATE_ELEM):
-        _need("gate", gate, gate.shape, R.dtype, R.device)
+        gs = gate.shape
+        if gs == (H,):
+            kind, col = L.LORA_GATE_COL, gate
+        elif gs == (T, 1):
+            kind = L.LORA_GATE_ROW
+        elif gs == shape:
+            kind = L.LORA_GATE_ELEM
+        else:
+            raise ValueError(f"gate has shape {tuple(gs)}, expected ({H},), ({T}, 1) or ({T}, {H})")
+        if col is None:
+            _need("gate", gate, gs, dtype, dev)
+    first = w_pre if w_pre is not None else w_post if w_post is not None else col
+    if first is not None:
+        pd = first.dtype
+        if pd != dtype:
+            torch = _torch()
+            if dtype != torch.bfloat16 or pd != torch.float32:
+                raise ValueError(f"parameters in {pd} with activations in {dtype} are not supported")
+            dt = L.LORA_BF16_F32LORA
+        if w_pre is not None:
+            _need("w_pre", w_pre, (H,), pd, dev)
+        if w_post is not None:
+            _need("w_post", w_post, (H,), pd, dev)
+        if col is not None:
+            _need("gate", col, (H,), pd, dev)
     return L.lora_norm_desc(T, H, eps, res_scale, branch_scale, int(unit_offset), kind, dt, 0)
 
 
@@ -760,31 +775,38 @@ def block_norm_bwd(dR_out, dX, R_out, Y=None, *, w_pre=None, w_post=None, gate=N
     forward had w_pre), its R_out and its Y.  Returns (dR, dY, grads): grads holds "w_pre", "w_post" and "gate"
     for those the forward had, each of its parameter's shape and dtype; dY is None without Y.  dR and dY may be
     given, and may be dR_out, dX, R_out or Y themselves."""
-    torch = _torch()
+    empty_like = _torch().empty_like
     d = _norm_call(R_out, Y, w_pre, w_post, gate, res_scale, branch_scale, eps, unit_offset)
-    for name, t, wanted in (("dR_out", dR_out, False), ("dX", dX, w_pre is not None), ("dR", dR, False), ("dY", dY, False)):
-        if t is not None or wanted:
-            _need(name, t, R_out.shape, R_out.dtype, R_out.device)
-    if dX is not None and w_pre is None:
+    shape, dtype, dev = R_out.shape, R_out.dtype, R_out.device
+    if w_pre is not None:
+        _need("dX", dX, shape, dtype, dev)
+    elif dX is not None:
         raise ValueError("dX needs w_pre")
-    if dY is not None and Y is None:
-        raise ValueError("dY needs Y")
-    params = {k: p for k, p in (("w_pre", w_pre), ("w_post", w_post), ("gate", gate)) if p is not None}
+    if dR_out is not None:
+        _need("dR_out", dR_out, shape, dtype, dev)
+    if dR is not None:
+        _need("dR", dR, shape, dtype, dev)
+    if dY is not None:
+        _need("dY", dY, shape, dtype, dev)
+        if Y is None:
+            raise ValueError("dY needs Y")
+    params = (("w_pre", w_pre), ("w_post", w_post), ("gate", gate))
     if grads is not None:
-        for k, p in params.items():
-            _need(f"grads[{k!r}]", grads.get(k), p.shape, p.dtype, R_out.device)
+        for k, p in params:
+            if p is not None:
+                _need(f"grads[{k!r}]", grads.get(k), p.shape, p.dtype, dev)
     _on_gpu(R_out, ws)
     with _on(stream):
-        dR = torch.empty_like(R_out) if dR is None else dR
-        if Y is not None and dY is None:
-            dY = torch.empty_like(Y)
+        if dR is None:
+            dR = empty_like(R_out)
+        if dY is None and Y is not None:
+            dY = empty_like(Y)
         if grads is None:
-            grads = {k: torch.empty_like(p) for k, p in params.items()}
-        if ws is None:
-            ws = _ws(block_norm_workspace_size(d.T, d.H, d.dtype), R_out.device)
-    gr = L.lora_norm_grads(*(_ptr(grads.get(k)) if k in params else None for k in ("gate", "w_post", "w_pre")))
-    _call_on(R_out, stream, "lora_block_norm_bwd", C.byref(d), _ptr(dR_out), _ptr(dX), _ptr(R_out), _ptr(Y), _ptr(gate),
-             _ptr(w_post), _ptr(w_pre), _ptr(dR), _ptr(dY), C.byref(gr), _ptr(ws), _nbytes(ws, R_out.device))
+            grads = {k: empty_like(p) for k, p in params if p is not None}
+        ws, ws_bytes = _work(ws, block_norm_workspace_size(d.T, d.H, d.dtype), dev)
+    gr = L.lora_norm_grads(*[None if p is None else grads[k].data_ptr() for k, p in reversed(params)])
+    _call_on(R_out, stream, "lora_block_norm_bwd", C.byref(d), _ptr(dR_out), _ptr(dX), R_out.data_ptr(), _ptr(Y),
+             _ptr(gate), _ptr(w_post), _ptr(w_pre), dR.data_ptr(), _ptr(dY), C.byref(gr), ws.data_ptr(), ws_bytes)
     return dR, dY, grads
 
 
