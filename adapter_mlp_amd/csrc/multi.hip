@@ -331,7 +331,8 @@ __global__ __launch_bounds__(256, BaseCfg<MT>::PER_CU) void multi_few_kernel(con
 // rows, each sorting the tile for itself, took longer to sort than to read X,
 // and A_i by loads into registers left each adapter a chain of latencies.)
 // Measured: 8192 rows of 4096 at rank 16, 67 MB of X: 23 us (2.9 TB/s); 777
-// rows of 14336 at rank 64 with 12 adapters: 26 us, the walk over the adapters.
+// rows of 14336 at rank 64 with 12 adapters: 18 to 22 us, the walk over the
+// adapters, which two blocks share (20 to 24 when both read the rows of the other).
 // ---------------------------------------------------------------------------
 // Rows of a 256-row tile in the order of their adapters (rows without one
 // last), by 256 threads: id_of and row_of hold the sorted ids and rows.
@@ -416,7 +417,7 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
   sort_tile(row_id(a, t0 + threadIdx.x), keys, id_of, row_of);
   slots_of_tile(id_of, heads, ids, slot, count);
   if (kc == 0 && blockIdx.z == 0) list_tile(a.plan[blockIdx.x], id_of, row_of, ids, slot, count, keys);
-  const int first = blockIdx.z, every = gridDim.z;  // this block's share of the adapters
+  const int first = blockIdx.z, every = gridDim.z;  // this block's share of the adapters: 1 or 2 blocks
   if (first >= count) return;                       // uniform over the block
   lds_char* const lds = (lds_char*)slices;
   auto issue = [&](int s, int buf) {
@@ -429,15 +430,16 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
   const brsrc rx = make_rsrc(static_cast<const char*>(a.X) + (t0 * a.K + k0) * 2, ((a.T - t0) * a.K - k0) * 2);
   int rslot[RG], row[RG];  // of this lane's MFMA rows
   u32x4 fx[RG][STEPS];
-  const bool any = __ballot(my >= 0) != 0;
+  // rows of this block's share (every is 1 or 2)
+  const bool any = __ballot(my >= 0 && (my & (every - 1)) == first) != 0;
 #pragma unroll
   for (int m = 0; m < RG; ++m) {
     rslot[m] = __shfl(my, 16 * m + c);
     row[m] = __shfl(myrow, 16 * m + c);
     const uint32_t at = (uint32_t)(row[m] * a.K * 2);
 #pragma unroll
-    for (int s = 0; s < STEPS; ++s)  // rows past T or without an adapter and K past the range read zero
-      fx[m][s] = buf_load16(rx, any && rslot[m] >= 0 && 32 * s < klen ? at + (uint32_t)(32 * s + 8 * g) * 2 : 0x80000000u);
+    for (int s = 0; s < STEPS; ++s)  // other rows (past T, without an adapter too) and K past the range read zero
+      fx[m][s] = buf_load16(rx, any && rslot[m] >= 0 && (rslot[m] & (every - 1)) == first && 32 * s < klen ? at + (uint32_t)(32 * s + 8 * g) * 2 : 0x80000000u);
   }
   issue(first, 0);
   int buf = 0;
