@@ -835,19 +835,28 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
 // Which path a bf16 call takes.  Few rows: W is streamed through 128-column
 // tiles with K split over the grid, and the adapters join the fp32 sums as
 // those are added up.  Many: the 256 x 256 tiles of the GEMM, with the adapters
-// in its epilogue.  A rule fitted to both, timed from 130 to 1536 rows (us, few
-// / many):
-//    4096 x 4096: 24 / 57 at 130 rows, 53 / 57 at 512, 60 / 59 at 640
-//    4096 x 14336: 49 / 62 at 130, 64 / 72 at 256, 92 / 84 at 300
-//    14336 x 4096: 48 / 96 at 130, 87 / 99 at 256, 114 / 103 at 300
-//    4096 x 1024: 47 / 52 at 777, 57 / 50 at 1024;  640 x 640: 23 / 37 at 1024
-// few grows as T K N / 3e8 + T K / 1.9e5 us, many starts at 38 + K / 213; up to
-// kFewRows rows always, and past 1024 never.
-constexpr int64_t kFewRows = 128;
-bool few_rows(int64_t T, int64_t K, int64_t N) {
-  if (T <= kFewRows || T > 1024) return T <= kFewRows;
-  const double t = (double)T, k = (double)K;
-  return t * k * ((double)N / 4.1e8 + 1 / 1.9e5) < 0.75 * (22 + k / 213);
+// in its epilogue.  The rule compares models of both, fitted to 900 shapes of
+// 136 to 3600 rows, 64 to 14336 wide, with 2 to 60 adapters of rank 16 to 64
+// (us; the choice is 3% from the faster of the two in the mean).  Few: X W, the
+// shrink of 16-row blocks that min(16, n) share, the parts' sum and U B. Many:
+// a longer start, the GEMM, and the walk over the adapters a 256-row tile
+// meets, counted as if the rows of all n came in runs, and at most 16: n is
+// what is loaded, not what the batch uses.  Measured, few / many:
+//    4096 x 4096, 12 of rank 32: 71 / 60 at 562 rows
+//    1664 x 192, 2 of rank 16: 17 / 46 at 1100, 33 / 50 at 4096
+//    1472 x 704, 2 of rank 16: 25 / 45 at 1536;  60 of rank 64: 69 / 64
+//    14336 x 4096, 2 of rank 16: 79 / 90 at 300, 125 / 97 at 562
+//    128 x 1664, 2 of rank 16: 23 / 25 at 1536, 32 / 25 at 2304
+// Up to kFewRows rows always few, past kManyRows always many.
+constexpr int64_t kFewRows = 128, kManyRows = 4096;
+int shrink_share(int64_t n);
+bool few_rows(const lora_multi_desc& d) {
+  if (d.T <= kFewRows || d.T > kManyRows) return d.T <= kFewRows;
+  const double t = (double)d.T, k = (double)d.K, n = (double)d.N, r = d.n ? (double)d.r : 0.0, z = shrink_share(d.n);
+  const double met = std::min(std::min((double)d.n, 16.0), 256.0 * (double)d.n / t + 1);
+  const double few = 15 + t / 1e6 * (k * (3.2e-3 * n + 1.35e-2 * z * r) + n * (2.1 + 3.2e-2 * r) + r * (29 + 8.8 * z));
+  const double many = 23 + k / 250 + t / 1e6 * (1.33e-3 * k * n + 35 * r) + met * (0.9 + r / 85);
+  return few < many;
 }
 
 // Row tiles of at most 128 rows, and the 16-row blocks of each.
@@ -941,7 +950,7 @@ struct MultiPlan {
 MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   MultiPlan p{};
   const bool bf16 = d.dtype == LORA_BF16;
-  p.few = base ? few_rows(d.T, d.K, d.N) : d.T <= kFewRows;
+  p.few = base ? few_rows(d) : d.T <= kFewRows;
   p.tiles = bf16 && base && !p.few;
   p.ks = !bf16 || !base || d.T == 0 ? 1 : p.tiles ? store_gemm_ksplit(d.T, d.N, d.K)
                                               : base_ksplit(d.T, d.K, d.N);

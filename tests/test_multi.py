@@ -73,7 +73,9 @@ def run(s, **kw):
 CASES = [(1, 64, 64, 8, 1), (1, 4096, 1024, 16, 3), (2, 128, 192, 16, 5), (16, 320, 576, 24, 7), (17, 1024, 128, 32, 40),
          (33, 1088, 704, 40, 4), (64, 512, 1024, 48, 9), (65, 4096, 512, 64, 80), (129, 2112, 320, 56, 6), (300, 576, 1088, 8, 300),
          (777, 1024, 640, 16, 12), (1030, 256, 2048, 64, 3), (2500, 512, 512, 32, 20),
-         (1300, 640, 320, 40, 300), (450, 4096, 4160, 16, 5), (1025, 64, 64, 8, 1), (1800, 192, 448, 56, 70)]
+         (1300, 640, 320, 40, 300), (450, 4096, 4160, 16, 5), (1025, 64, 64, 8, 1), (1800, 192, 448, 56, 70),
+         (2304, 640, 640, 24, 2), (4096, 1664, 192, 16, 1), (3000, 2112, 704, 64, 9), (4097, 64, 64, 8, 1), (4100, 128, 192, 40, 5),
+         (4500, 192, 448, 56, 70), (4300, 640, 320, 32, 300), (800, 4096, 2112, 48, 6)]
 
 
 @pytest.mark.gpu
@@ -93,7 +95,7 @@ def test_f32(T, K, N, r, n, ids):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 20, 700])
+@pytest.mark.parametrize("T", [1, 20, 700, 4200])
 def test_added_to_a_base(T):
     s = make(T, 1024, 512, 16, 6)
     base = run(make(T, 1024, 512, 16, 6, ids="none"))
@@ -109,7 +111,7 @@ def test_added_to_a_base(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,K,N,r", [(300, 14336, 64, 64), (129, 2048, 64, 8), (128, 2048, 64, 8), (1100, 320, 64, 40)])
+@pytest.mark.parametrize("T,K,N,r", [(300, 14336, 64, 64), (129, 2048, 64, 8), (128, 2048, 64, 8), (1100, 320, 64, 40), (4200, 320, 64, 40)])
 def test_one_workspace_for_both_forms(T, K, N, r):
     """The size that is asked for covers the call without W too, whichever path the one with W takes."""
     s = make(T, K, N, r, 5)
@@ -130,7 +132,7 @@ def test_beside_an_nf4_base():
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [1, 40, 900, 1100])
+@pytest.mark.parametrize("T", [1, 40, 900, 1100, 4200])
 def test_one_adapter_agrees_with_o_fwd(T):
     s = make(T, 512, 768, 16, 3, ids="one")
     p = s["pool"]
@@ -140,7 +142,7 @@ def test_one_adapter_agrees_with_o_fwd(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [9, 80, 1000, 1200])
+@pytest.mark.parametrize("T", [9, 80, 1000, 1200, 4200])
 def test_a_bad_adapter_or_row_stays_alone(T):
     s = make(T, 512, 512, 24, 8)
     want = run(s)
@@ -164,7 +166,7 @@ def test_no_rows_and_no_adapters(dtype):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [5, 100, 600, 1500])
+@pytest.mark.parametrize("T", [5, 100, 600, 1500, 4200])
 def test_other_stream_and_same_answer(T):
     s = make(T, 1024, 1024, 16, 7)
     want = run(s)
@@ -178,7 +180,7 @@ def test_other_stream_and_same_answer(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [3, 90, 500, 1300])
+@pytest.mark.parametrize("T", [3, 90, 500, 1300, 4200])
 def test_captured_graph_replays(T):
     s = make(T, 512, 576, 16, 6)
     Y = run(s)
@@ -197,7 +199,7 @@ def test_captured_graph_replays(T):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [4, 700, 1100])
+@pytest.mark.parametrize("T", [4, 700, 1100, 4200])
 def test_stacks_past_two_gib(T):
     s = make(T, 64, 128, 64, 2, ids="each")
     n = 1 << 18
