@@ -626,7 +626,7 @@ def _call_on(t, stream, name, *args):
             L.call(name, *args, raw)
 
 
-def _work(ws, need, dev):
+def _ws_for(ws, need, dev):
     """The workspace of a call and its size: the caller's (as _on_gpu has checked it) or a new one."""
     if ws is not None:
         return ws, ws.numel() * ws.element_size()
@@ -680,7 +680,7 @@ def multi_fwd(X, W, pool: AdapterPool, ids, *, Y=None, ws=None, stream=None):
     with _on(stream):
         if Y is None:
             Y = torch.empty((T, N), dtype=X.dtype, device=dev)
-        ws, ws_bytes = _work(ws, multi_workspace_size(T, K, N, r, n, dt), dev)
+        ws, ws_bytes = _ws_for(ws, multi_workspace_size(T, K, N, r, n, dt), dev)
     _call_on(X, stream, "lora_multi_fwd", C.byref(d), X.data_ptr(), _ptr(W), A.data_ptr(), B.data_ptr(),
              pool.scale.data_ptr(), ids.data_ptr(), Y.data_ptr(), ws.data_ptr(), ws_bytes)
     return Y
@@ -803,7 +803,7 @@ def block_norm_bwd(dR_out, dX, R_out, Y=None, *, w_pre=None, w_post=None, gate=N
             dY = empty_like(Y)
         if grads is None:
             grads = {k: empty_like(p) for k, p in params if p is not None}
-        ws, ws_bytes = _work(ws, block_norm_workspace_size(d.T, d.H, d.dtype), dev)
+        ws, ws_bytes = _ws_for(ws, block_norm_workspace_size(d.T, d.H, d.dtype), dev)
     gr = L.lora_norm_grads(*[None if p is None else grads[k].data_ptr() for k, p in reversed(params)])
     _call_on(R_out, stream, "lora_block_norm_bwd", C.byref(d), _ptr(dR_out), _ptr(dX), R_out.data_ptr(), _ptr(Y),
              _ptr(gate), _ptr(w_post), _ptr(w_pre), dR.data_ptr(), _ptr(dY), C.byref(gr), ws.data_ptr(), ws_bytes)
