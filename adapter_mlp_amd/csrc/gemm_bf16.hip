@@ -1613,10 +1613,11 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
   }
 
   // ---- adapters per row (MULTI) ----
-  // Once the operand slots are free: the tile's rows of U [M, 64] go to an
-  // activation slot, once; then for each adapter of the tile, B_i (its r rows,
-  // zeros up to a multiple of 32) goes through the weight ring, is multiplied
-  // with the 16-row blocks that hold rows of it, and
+  // Once the operand slots are free: the tile's rows of U (a high and a low
+  // bf16 part, see multi_u_kernel) go to the activation slots, once; then for
+  // each adapter of the tile, B_i (its r rows, zeros up to a multiple of 32)
+  // goes through the weight ring, both parts of the 16-row blocks that hold
+  // rows of it are multiplied with it, and
   // the products are added where the row (one per lane) is its own.  Selecting
   // instead of multiplying by zeros keeps an adapter that holds infinities to
   // its own rows, and costs eight vector instructions per two MFMAs in the
@@ -1665,11 +1666,16 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
         }
       }
       if (count > 0) {
-        const i32x4 ru = rsrc_words(static_cast<const char*>(args.mt_u) + m0 * 128, (M - m0) * 128);
+        // slot 0: high and low parts in one row of 64 (rank <= 32), or the high parts, with the low ones in slot 1
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dma16(ru, (uint32_t)((8 * (4 * wave + i) + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)),
-                lds_addr(lds) + (4 * wave + i) * 1024);
+        for (int h = 0; h < 2; ++h)
+          if (h < ksteps) {
+            const i32x4 ru = rsrc_words(static_cast<const char*>(args.mt_u) + (h * M + m0) * 128, (M - m0) * 128);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dma16(ru, (uint32_t)((8 * (4 * wave + i) + (lane >> 3)) * 128 + (((lane & 7) ^ (lane >> 3)) << 4)),
+                    lds_addr(lds) + h * SLOT_BYTES + (4 * wave + i) * 1024);
+          }
         issue_b(0, __builtin_amdgcn_readlane(ids, 0));
         for (int s = 0; s < count; ++s) {
           const uint32_t rows = (uint32_t)__builtin_amdgcn_readlane(blk, s & 63) >> (8 * wm);
@@ -1696,13 +1702,42 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
             const bool own = sl[j] == s;
             const bf16x8 u0 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(0, j)] + 2048 * j));
             const bf16x8 u1 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(1, j)] + 2048 * j));
+            f32x4 d[4];
+            if (ksteps == 2) {
+              const bf16x8 l0 = __builtin_bit_cast(bf16x8, lds_read16(lds + SLOT_BYTES + ao[kc16_at(0, j)] + 2048 * j));
+              const bf16x8 l1 = __builtin_bit_cast(bf16x8, lds_read16(lds + SLOT_BYTES + ao[kc16_at(1, j)] + 2048 * j));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              f32x4 d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, f32x4{0, 0, 0, 0}, 0, 0, 0);
-              if (ksteps == 2) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], u1, d, 0, 0, 0);
+              for (int i = 0; i < 4; ++i) {
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], l0, f32x4{0, 0, 0, 0}, 0, 0, 0);
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], l1, d[i], 0, 0, 0);
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, d[i], 0, 0, 0);
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], u1, d[i], 0, 0, 0);
+              }
+            } else {
 #pragma unroll
-              for (int v = 0; v < 4; ++v) acc[i][j][v] = own ? acc[i][j][v] + d[v] : acc[i][j][v];
+              for (int i = 0; i < 4; ++i) {
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u1, f32x4{0, 0, 0, 0}, 0, 0, 0);
+                d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, d[i], 0, 0, 0);
+              }
             }
+            // An infinity in B_i times a low part that is zero or has the other sign gives NaN where the
+            // product with U is infinite: there the high parts alone say which infinity it is.
+            float all = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) all += (d[i][0] + d[i][1]) + (d[i][2] + d[i][3]);
+            if (__ballot(all != all) != 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f32x4 h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, f32x4{0, 0, 0, 0}, 0, 0, 0);
+                if (ksteps == 2) h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], u1, h, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) d[i][v] = d[i][v] != d[i][v] ? h[v] : d[i][v];
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[i][j][v] = own ? acc[i][j][v] + d[i][v] : acc[i][j][v];
           }
         }
         __syncthreads();  // the slots become epilogue staging

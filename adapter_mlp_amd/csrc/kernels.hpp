@@ -121,8 +121,10 @@ struct GemmArgs {
   int32_t rc_R, pad5_;
   // EPI_STORE, bf16, dense NN, one region, with mt_plan set: each row's own
   // adapter is added to the sums before they are rounded: row m takes
-  // U[m] B_i, U = mt_u [M, 64] (scaled, zero past the rank), B_i = mt_b [n, mt_r, N],
-  // i by the plan of the row's 256-row tile (MultiTile).
+  // U[m] B_i, B_i = mt_b [n, mt_r, N], i by the plan of the row's 256-row tile
+  // (MultiTile).  U (scaled) is the sum of a high and a low bf16 part, zero past
+  // the rank: mt_u [M, 64] holds the high ones in columns 0 .. 31 and the low
+  // ones in 32 .. 63 up to rank 32, above that mt_u [2][M, 64] one after the other.
   const void* mt_u;
   const void* mt_b;
   const struct MultiTile* mt_plan;

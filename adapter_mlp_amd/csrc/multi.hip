@@ -21,7 +21,7 @@ struct MultiArgs {
   int64_t T, K, N, n;
   int32_t r, ks, kc, ntn, ntm;
   int32_t nshrink, nz;  // few rows: blocks of the shrink, and how many share the adapters of 16 rows
-  uint16_t* u;          // [T, 64] bf16: scaled U, zero past the rank (many rows)
+  uint16_t* u;          // scaled U in two bf16 parts, as GemmArgs::mt_u (many rows)
   MultiTile* plan;      // adapters of every 256-row tile (many rows)
 };
 
@@ -475,8 +475,12 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
   }
 }
 
-// U of many rows as the GEMM reads it: summed over the K ranges, scaled and
-// rounded to bf16 (as the one-adapter calls do).  Four rows a block: lane 8 k +
+// U of many rows as the GEMM reads it: summed over the K ranges, scaled, and
+// split into two bf16 parts, u = hi + lo + e with |e| <= 2^-16 |u|: the matrix
+// cores take bf16, and one part alone would make a row's result depend on how
+// many rows share its batch by half a bf16 step of U (the few-rows path keeps
+// U in fp32); what two parts leave is 1/256 of the output's own rounding.
+// Four rows a block: lane 8 k +
 // j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
 // and the eight sums of a column meet by a butterfly, so that the loads of 56
 // ranges (K = 14336) are two round trips.  5 to 7 us at both sizes above.
@@ -515,9 +519,18 @@ __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
       s0[i] += __shfl_xor(s0[i], d);
       s1[i] += __shfl_xor(s1[i], d);
     }
-  if (k0 == 0)
-    *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) =
-        u32x4{pack_bf2(s0[0], s0[1]), pack_bf2(s0[2], s0[3]), pack_bf2(s1[0], s1[1]), pack_bf2(s1[2], s1[3])};
+  if (k0 == 0 && (a.r > 32 || j0 < 32)) {
+    u32x4 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x = i < 2 ? s0[2 * i] : s1[2 * i - 4], y = i < 2 ? s0[2 * i + 1] : s1[2 * i - 3];
+      hi[i] = pack_bf2(x, y);
+      const float p = lo_bf(hi[i]), q = hi_bf(hi[i]);  // an infinity or NaN has no low part
+      lo[i] = pack_bf2(__builtin_isfinite(p) ? x - p : 0.0f, __builtin_isfinite(q) ? y - q : 0.0f);
+    }
+    *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) = hi;
+    *reinterpret_cast<u32x4*>(a.u + (a.r > 32 ? (a.T + t) * 64 : t * 64 + 32) + j0) = lo;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -957,7 +970,7 @@ MultiPlan plan_multi(const lora_multi_desc& d, bool base, void* ws) {
   p.kc = bf16 ? shrink_ranges(p.few, d.K) : 1;
   Ws w(ws);
   p.upart = static_cast<float*>(w.take((size_t)p.kc * d.T * d.r * 4));
-  if (p.tiles) p.u = static_cast<uint16_t*>(w.take((size_t)d.T * 128));
+  if (p.tiles) p.u = static_cast<uint16_t*>(w.take((size_t)d.T * (d.r > 32 ? 256 : 128)));
   if (bf16 && !p.few) p.plan = static_cast<MultiTile*>(w.take((size_t)cdiv(d.T, 256) * sizeof(MultiTile)));
   if (bf16 && base && (!p.tiles || p.ks > 1)) p.part = static_cast<float*>(w.take((size_t)p.ks * d.T * d.N * 4));
   p.bytes = w.off;

@@ -228,6 +228,46 @@ def test_more_rows_than_a_grid_row(K, N, r):
     assert torch.equal(got[full:], want[:T - full])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [8, 24, 32, 40, 64])
+@pytest.mark.parametrize("T", [70, 1000, 4200])
+def test_adapter_term_alone_keeps_its_bits(T, r):
+    """Without a base (W = 0) what is left is U B_i.  However many rows share the batch, U loses no more
+    than two bf16 parts leave of it: each rounds by half a step, 2^-8 2^-8 = 2^-16 of U."""
+    K, N = 512, 512
+    s = make(T, K, N, r, 5)
+    s["W"].zero_()
+    X, ids, p, c = s["X"].double().cpu(), s["ids"].cpu().long(), s["pool"], (K / 32 + 16) * 2.0 ** -24
+    y, mag = torch.zeros(T, N).double(), torch.zeros(T, N).double()
+    for i in range(5):
+        rows = torch.nonzero(ids == i).flatten()
+        A, B, k = p.A[i].double().cpu(), p.B[i].double().cpu(), float(p.scale[i])
+        U = X[rows] @ A
+        y[rows] = k * (U @ B)
+        mag[rows] = k * ((c * (X[rows].abs() @ A.abs()) + (2.0 ** -16 + (r + 2) * 2.0 ** -24) * U.abs()) @ B.abs())
+    check(run(s), (y, HALF[torch.bfloat16] * y.abs() * (1 + 2.0 ** -7) + mag))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [16, 64])
+@pytest.mark.parametrize("T", [40, 1000, 4200])
+def test_an_infinite_weight_gives_its_infinity(T, r):
+    """One infinity in a column of B_3: the rows of that adapter are infinite there, with the sign of their U."""
+    s = make(T, 512, 512, r, 5)
+    s["X"][::2] = 0.0
+    s["X"][::2, 0] = 1.0                                # U of these rows is A's first row, a bf16 value: no low part
+    s["pool"].scale.fill_(1.0)
+    want = run(s)
+    s["pool"].B[3, 5, 100] = float("inf")
+    got = run(s)
+    rows = (s["ids"] == 3).nonzero().flatten()
+    U = s["X"][rows].double().cpu() @ s["pool"].A[3, :, 5].double().cpu()
+    assert len(rows) and (U.abs() > 1e-4).all()         # far from where the fp32 sums could change a sign
+    assert torch.equal(got[rows, 100].double().cpu(), U.sign() * float("inf"))
+    got[rows, 100] = want[rows, 100]
+    assert torch.equal(got, want)
+
+
 # ---- refusals (no GPU) ----
 
 def test_binding_refuses():
