@@ -114,6 +114,27 @@ def test_zero_deficient_extreme_and_bad_matrices():
     check("eps", lm.orthogonalize(G[:5]), torch.cat([torch.zeros(1, 500, 16).double(), ns64(G[1:5])]))
 
 
+# The most steps that each set of coefficients is taken to: |a|^steps <= 2^22.
+MOST = [(12, lm.NS_COEFFS), (22, (2.0, -1.5, 0.5)), (24, (1.875, -1.25, 0.375)), (32, (1.5, -0.5, 0.0))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [16, 20, 40, 64])
+@pytest.mark.parametrize("steps,coeffs", MOST)
+def test_deficient_matrices_at_the_most_steps(steps, coeffs, r):
+    """Gradients of fewer tokens than the rank: no singular value where rounding leaves 2^-53 in the Gram
+    matrix, which each step multiplies by a^2.  An entry may be off by that."""
+    g = torch.Generator().manual_seed(r)
+    G = rnd((4, 700, r), device="cpu")
+    G[0, :, r // 2] = G[0, :, r // 2 - 1]
+    G[1] = torch.randint(-8, 9, (700, 1), generator=g) * torch.arange(1, r + 1)  # rank 1, exact in fp32
+    G[2] = (torch.randint(-8, 9, (700, 3), generator=g) @ torch.randint(-8, 9, (3, r), generator=g)).float()
+    G = G.cuda()
+    slack = 2.0 ** -53 * coeffs[0] ** (2 * steps)
+    for mats in (G, G.transpose(1, 2).contiguous()):
+        check("deficient", lm.orthogonalize(mats, steps=steps, coeffs=coeffs), ns64(mats, steps, coeffs), slack)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("r", [4, 20, 40, 64])
 def test_zeros_without_eps(r):
