@@ -864,7 +864,8 @@ def orthogonalize(mats, *, steps=5, coeffs=NS_COEFFS, eps=1e-7, out=None, ws=Non
     """Newton-Schulz steps X <- a X + (b S + c S S) X, S = X X^T, from X = G / (|G| + eps), for every matrix of
     ``mats``: one tensor or a list of them, each [rows, cols] or a stack [count, rows, cols] with one side at
     most 64 (adapters or their gradients), bf16 or fp32.  Returns the same structure; ``out`` (or mats itself)
-    receives the results."""
+    receives the results.  |a|^steps may not exceed 2^22 (12 steps of the default coefficients), where the rounding
+    of fp64 would reach the result."""
     torch = _torch()
     one = torch.is_tensor(mats)
     G = _stacks("mats", mats)

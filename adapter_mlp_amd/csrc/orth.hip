@@ -45,6 +45,16 @@ constexpr int kRegion = 2560 + 64;   // floats of LDS a wavefront holds them in
 // than 2^30 long-side elements in all has fewer blocks than that (a sub-tile has at least 32 of them).
 constexpr int64_t kMaxBlocks = (1 << 24) - 1, kMaxMats = (1 << 22) - 1, kMaxLong = 1 << 30;
 
+// Where U has (nearly) no singular value, rounding leaves +-2^-53 |G| in G, and
+// every step multiplies it by a^2.  Once it is of order one a negative value
+// makes p(g) exceed a, and G and Q run away (from 16 steps on with the default
+// coefficients, for gradients of fewer tokens than the rank).  Up to there the
+// error of an entry of O (entries are about 1 at most) is below 2^-53 a^(2 steps):
+// measured at most 0.007 of it for five sets of coefficients, ranks 16 to 64, full,
+// steep and deficient spectra.  At |a|^steps = 2^22 that is 2^-9, measured 8e-6:
+// 12 steps of the default coefficients, 22 at a = 2, 32 at a = 1.5.
+constexpr double kMaxGrowth = 1 << 22;
+
 // One stack of `count` matrices with the same shape.
 struct OrthGroup {
   const void* G;
@@ -354,7 +364,8 @@ __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const O
 // out), 9 us at rank 16 (0.9 a step, a chain of products), whatever the number
 // of matrices up to the chip's CUs.
 // fp32 products would halve the steps and lose the small singular values: an error
-// of 2^-24 |G| in a direction of G's null space grows by a^2 a step.
+// of 2^-24 |G| in a direction of G's null space grows by a^2 a step.  In fp64 it is
+// 2^-53 |G|, and kMaxGrowth keeps it small.
 template <int NT>
 __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, NP = NT * (NT + 1) / 2, THREADS = NT >= 3 ? 1024 : 256 * NT;
@@ -663,6 +674,8 @@ lora_status check_orth(const lora_orth_desc* d, const lora_orth_mat* mats) {
   CHECK(d->n >= 0 && (d->n == 0 || mats != nullptr), LORA_EINVAL, "%d matrices at NULL", d->n);
   CHECK(d->steps >= 1 && d->steps <= 32, LORA_EINVAL, "steps = %d is not in [1, 32]", d->steps);
   CHECK(std::isfinite(d->a) && std::isfinite(d->b) && std::isfinite(d->c), LORA_EINVAL, "a coefficient is not finite");
+  CHECK(std::pow(std::fabs(d->a), d->steps) <= kMaxGrowth, LORA_EINVAL,
+        "%d steps with a = %g multiply rounding errors by more than 2^44", d->steps, d->a);
   CHECK(std::isfinite(d->eps) && d->eps >= 0.0, LORA_EINVAL, "eps must be finite and not negative");
   CHECK(d->reserved == 0, LORA_EINVAL, "reserved must be 0");
   for (int i = 0; i < d->n; ++i) {

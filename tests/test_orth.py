@@ -242,6 +242,19 @@ def test_binding_refuses():
     bad(lm.muon_step, [G], [G], [M], lr=0.1, scale=[1.0, 2.0])
 
 
+@pytest.mark.parametrize("steps,coeffs", [m for m in MOST if m[0] < 32] + [(1, (2.0 ** 22, 0.0, 0.0)), (2, (-2.0 ** 11, 0.0, 0.0))])
+def test_refuses_steps_that_grow_rounding_errors(steps, coeffs):
+    mat = L.lora_orth_mat(1 << 20, None, 2 << 20, 1, 100, 8, 1.0, 0)
+    size = ctypes.c_size_t()
+    for k, want in ((steps, L.LORA_OK), (steps + 1, L.LORA_EINVAL), (32, L.LORA_EINVAL)):
+        d = L.lora_orth_desc(1, k, *coeffs, 1e-7, L.LORA_F32, 0)
+        assert L.load().lora_orth_workspace_size(ctypes.byref(d), ctypes.byref(mat), ctypes.byref(size)) == want
+    muon = L.lora_muon_desc(L.lora_orth_desc(1, steps + 1, *coeffs, 1e-7, L.LORA_F32, 0), 0.1, 0.9, 0.0, 1, 0)
+    mat.M = 3 << 20
+    assert L.load().lora_muon_step(ctypes.byref(muon), ctypes.byref(mat), 1 << 30, 1 << 40, None) == L.LORA_EINVAL
+    assert L.load().lora_orthogonalize(ctypes.byref(muon.orth), ctypes.byref(mat), 1 << 30, 1 << 40, None) == L.LORA_EINVAL
+
+
 def test_library_refuses():
     """Refused on the host; no address here is read."""
     def call(muon=False, mats=((1, 2, 0, 1, 100, 8, 1.0, 0),), steps=5, a=1.0, eps=1e-7, dtype=L.LORA_F32, n=None, lr=0.1,
