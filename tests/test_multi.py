@@ -268,6 +268,60 @@ def test_an_infinite_weight_gives_its_infinity(T, r):
     assert torch.equal(got, want)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("ids", ["mixed", "runs"])
+@pytest.mark.parametrize("T,K,N,r,n", [(1500, 1030, 1500, 51, 6), (2053, 512, 1055, 16, 3), (1601, 77, 1344, 7, 9)])
+def test_f32_of_whole_tiles(T, K, N, r, n, ids):
+    """512 blocks of 64 x 64 and more: the form that does not split K, through its pipelined steps and its tail."""
+    s = make(T, K, N, r, n, "f32", ids)
+    check(run(s), reference(s))
+    base = torch.randn(T, N, generator=torch.Generator().manual_seed(1)).cuda()
+    check(lm.multi_fwd(s["X"], None, s["pool"], s["ids"], Y=base.clone()), reference(s, base))
+
+
+def shifted(t):
+    """The same values one element past a 16-byte boundary."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    out = flat[1:].view(t.shape)
+    assert out.data_ptr() % 16 == 4
+    return out.copy_(t)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r", [(9, 256, 128, 8), (130, 333, 129, 20), (1500, 128, 1536, 16)])
+def test_f32_at_four_byte_addresses(T, K, N, r):
+    s = make(T, K, N, r, 4, "f32")
+    want = run(s)
+    p = s["pool"]
+    q = dict(s, X=shifted(s["X"]), W=shifted(s["W"]), pool=lm.AdapterPool(A=shifted(p.A), B=shifted(p.B), scale=shifted(p.scale)),
+             ids=shifted(s["ids"]))
+    assert torch.equal(run(q, Y=shifted(torch.zeros(T, N, device="cuda"))), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [16, 40])
+def test_split_and_unsplit_tiles_in_one_launch(r):
+    """272 tiles of 256 x 256 on 256 CUs: the last 16 are split over K, and take their adapters in the first part."""
+    T, K, N, n = 4349, 8192, 4096, 5
+    g = torch.Generator(device="cuda").manual_seed(r)
+
+    def rnd(*shape, scale=1.0):
+        return (torch.randn(shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
+
+    s = dict(X=rnd(T, K), W=rnd(K, N, scale=K ** -0.5), ids=torch.randint(-1, n, (T,), generator=g, device="cuda", dtype=torch.int32))
+    p = s["pool"] = lm.AdapterPool(A=rnd(n, K, r, scale=K ** -0.5), B=rnd(n, r, N, scale=r ** -0.5),
+                                   scale=torch.rand(n, generator=g, device="cuda") + 0.5)
+    X, W, c = s["X"].double(), s["W"].double(), (K / 32 + 16) * 2.0 ** -24
+    y, mag = X @ W, c * (X.abs() @ W.abs())
+    for i in range(n):
+        rows = torch.nonzero(s["ids"] == i).flatten()
+        A, B, k = p.A[i].double(), p.B[i].double(), float(p.scale[i])
+        U = X[rows] @ A
+        y[rows] += k * (U @ B)
+        mag[rows] += k * ((c * (X[rows].abs() @ A.abs()) + (2.0 ** -16 + (r + 2) * 2.0 ** -24) * U.abs()) @ B.abs())
+    check(run(s), (y.cpu(), (HALF[torch.bfloat16] * y.abs() * (1 + 2.0 ** -7) + mag).cpu()))
+
+
 # ---- refusals (no GPU) ----
 
 def test_binding_refuses():
