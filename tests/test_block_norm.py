@@ -295,6 +295,41 @@ def test_past_two_gib():
     check_bwd(s, (dR[-3:], dY[-3:], grads))
 
 
+# More rows than blocks at every number of threads a row, with values in all of them: the rows that a block
+# takes one after the other meet in its registers and in LDS.
+DEEP = [("bf16", 4500, 576), ("bf16", 2100, 4096), ("bf16", 1100, 5120), ("bf16", 1100, 5184), ("bf16", 1100, 6144),
+        ("bf16", 1100, 8192), ("bf16", 1100, 12288), ("bf16_f32", 1100, 5184), ("bf16_f32", 1100, 8192), ("bf16_f32", 1100, 16384),
+        ("f32", 4500, 700), ("f32", 4500, 701), ("f32", 1100, 1025), ("f32", 1100, 2049), ("f32", 1100, 4095),
+        ("f32", 1100, 5001), ("f32", 1100, 9001), ("f32", 1100, 4100), ("f32", 1100, 8196), ("f32", 1100, 16384)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["col", "elem"])
+@pytest.mark.parametrize("mode,T,H", DEEP)
+def test_more_rows_than_blocks(mode, T, H, gate):
+    s = make(T, H, mode, gate, True, True, seed=T + H)
+    check_fwd(s, run_fwd(s))
+    check_bwd(s, run_bwd(s))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["none", "col", "row", "elem"])
+@pytest.mark.parametrize("T,H", [(33, 64), (1100, 1028), (5, 8192)])
+def test_f32_at_four_byte_addresses(T, H, gate):
+    def shifted(t):
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t) if torch.is_tensor(t) else t
+
+    s = make(T, H, "f32", gate, True, True)
+    q = {k: shifted(v) for k, v in s.items()}
+    q["par"] = {k: shifted(v) for k, v in s["par"].items()}
+    assert q["R"].data_ptr() % 16 == 4
+    check_fwd(q, run_fwd(q))
+    check_bwd(q, run_bwd(q))
+    one = dict(s, Y=q["Y"])  # one tensor of the call is enough
+    check_fwd(one, run_fwd(one))
+    check_bwd(one, run_bwd(one))
+
+
 # ---- refusals (no GPU) ----
 
 def test_binding_refuses():
