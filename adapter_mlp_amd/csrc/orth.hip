@@ -352,10 +352,11 @@ __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const O
 // p = a I + b G + c G G; V = G p and Q <- Q p; G <- V p.  All matrices are
 // symmetric and commute, so both operands of a product are read along rows,
 // and only the tiles on and above the diagonal are formed (10 of 16 at NT =
-// 4) and written to both sides; in a tile on the diagonal too only what stands
-// on or above it counts, because rounding that is not symmetric grows by a^3 a
-// step instead of a^2.  A matrix has only its CU's matrix cores, 2048
-// flops in 64 cycles each, and at NT = 4 that is the bound: one tile a
+// 4) and written to both sides.  G is made symmetric to the last bit, in tiles
+// on the diagonal too (p then is, as its elements are the same sums): in G and p
+// rounding that is not symmetric would grow by a^3 a step instead of a^2.  A
+// matrix has only its CU's matrix cores, 2048 flops in 64 cycles each, and at NT =
+// 4 that is the bound: one tile a
 // wavefront, so that the four matrix cores share each product evenly and one
 // wavefront's LDS reads hide behind another's MFMAs.  Rows are 16 NT + 2
 // doubles apart, which spreads the 16 rows of a fragment read over all banks.
@@ -431,7 +432,8 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
   };
   auto put = [&](double* D, int t, int s, int v, double x) {
     const int row = 16 * t + 4 * v + q, col = 16 * s + c;
-    if (row <= col) D[row * LD + col] = D[col * LD + row] = x;
+    D[row * LD + col] = x;
+    if (t != s) D[col * LD + row] = x;
   };
   constexpr int MOST = (2 * NP + WAVES - 1) / WAVES;  // tiles of a pair of products per wavefront
   f64x4 x[MOST];
@@ -479,7 +481,10 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
       corner(i, t, s);
       const f64x4 o = product(mv, mp, t, s);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) put(mg, t, s, v, o[v]);
+      for (int v = 0; v < 4; ++v) {
+        const int row = 16 * t + 4 * v + q, col = 16 * s + c;
+        if (row <= col) mg[row * LD + col] = mg[col * LD + row] = o[v];
+      }
     }
     __syncthreads();
   }
