@@ -322,6 +322,23 @@ def test_split_and_unsplit_tiles_in_one_launch(r):
     check(run(s), (y.cpu(), (HALF[torch.bfloat16] * y.abs() * (1 + 2.0 ** -7) + mag).cpu()))
 
 
+@pytest.mark.gpu
+def test_current_stream_without_the_internal_accessor(monkeypatch):
+    s = make(5, 256, 128, 8, 3)
+    want = run(s)
+    torch.cuda.synchronize()
+    side, dev = torch.cuda.Stream(), s["X"].device
+    for missing in (False, True):
+        if missing:
+            monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+        assert lm._current_stream(dev) == torch.cuda.current_stream(dev).cuda_stream
+        with torch.cuda.stream(side):
+            assert lm._current_stream(dev) == side.cuda_stream
+            got = run(s)
+        side.synchronize()
+        assert torch.equal(got, want)
+
+
 # ---- refusals (no GPU) ----
 
 def test_binding_refuses():
