@@ -1702,7 +1702,7 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
             const bool own = sl[j] == s;
             const bf16x8 u0 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(0, j)] + 2048 * j));
             const bf16x8 u1 = __builtin_bit_cast(bf16x8, lds_read16(lds + ao[kc16_at(1, j)] + 2048 * j));
-            f32x4 d[4];
+            f32x4 d[4];  // low parts first
             if (ksteps == 2) {
               const bf16x8 l0 = __builtin_bit_cast(bf16x8, lds_read16(lds + SLOT_BYTES + ao[kc16_at(0, j)] + 2048 * j));
               const bf16x8 l1 = __builtin_bit_cast(bf16x8, lds_read16(lds + SLOT_BYTES + ao[kc16_at(1, j)] + 2048 * j));
@@ -1718,20 +1718,6 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
               for (int i = 0; i < 4; ++i) {
                 d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u1, f32x4{0, 0, 0, 0}, 0, 0, 0);
                 d[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, d[i], 0, 0, 0);
-              }
-            }
-            // An infinity in B_i times a low part that is zero or has the other sign gives NaN where the
-            // product with U is infinite: there the high parts alone say which infinity it is.
-            float all = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) all += (d[i][0] + d[i][1]) + (d[i][2] + d[i][3]);
-            if (__ballot(all != all) != 0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f32x4 h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[i], u0, f32x4{0, 0, 0, 0}, 0, 0, 0);
-                if (ksteps == 2) h = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[4 + i], u1, h, 0, 0, 0);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) d[i][v] = d[i][v] != d[i][v] ? h[v] : d[i][v];
               }
             }
 #pragma unroll

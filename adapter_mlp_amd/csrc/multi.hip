@@ -480,6 +480,9 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
 // cores take bf16, and one part alone would make a row's result depend on how
 // many rows share its batch by half a bf16 step of U (the few-rows path keeps
 // U in fp32); what two parts leave is 1/256 of the output's own rounding.
+// hi is cut off and lo rounded, so that both have u's sign and an infinity in B_i
+// is multiplied into the same infinity twice; a low part of zero, which would give
+// NaN there, is the smallest normal number instead, 2^-16 of u at most.
 // Four rows a block: lane 8 k +
 // j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
 // and the eight sums of a column meet by a butterfly, so that the loads of 56
@@ -523,10 +526,21 @@ __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
     u32x4 hi, lo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = i < 2 ? s0[2 * i] : s1[2 * i - 4], y = i < 2 ? s0[2 * i + 1] : s1[2 * i - 3];
-      hi[i] = pack_bf2(x, y);
-      const float p = lo_bf(hi[i]), q = hi_bf(hi[i]);  // an infinity or NaN has no low part
-      lo[i] = pack_bf2(__builtin_isfinite(p) ? x - p : 0.0f, __builtin_isfinite(q) ? y - q : 0.0f);
+      float l[2];
+      uint32_t h[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float x = i < 2 ? s0[2 * i + k] : s1[2 * i - 4 + k];
+        h[k] = __float_as_uint(x) & 0xffff0000u;
+        const float d = x - __uint_as_float(h[k]);
+        l[k] = d == 0.0f && fabsf(x) >= 0x1p-110f ? copysignf(0x1p-126f, x) : d;
+        if (!__builtin_isfinite(x)) {
+          h[k] = f2bf(x) << 16;
+          l[k] = x;
+        }
+      }
+      hi[i] = (h[0] >> 16) | h[1];
+      lo[i] = pack_bf2(l[0], l[1]);
     }
     *reinterpret_cast<u32x4*>(a.u + t * 64 + j0) = hi;
     *reinterpret_cast<u32x4*>(a.u + (a.r > 32 ? (a.T + t) * 64 : t * 64 + 32) + j0) = lo;
