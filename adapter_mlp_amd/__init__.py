@@ -643,7 +643,8 @@ def _ws_for(ws, need, dev):
 
 @dataclass
 class AdapterPool:
-    """Adapters of one projection, stacked: A [n, n_in, r], B [n, r, n_out] and their scales [n] (fp32)."""
+    """Adapters of one projection, stacked: A [n, n_in, r], B [n, r, n_out] and their scales [n] (fp32).
+    A and B have the type of the activations (adapters trained in fp32 beside bf16 are cast once, here)."""
 
     A: object
     B: object
@@ -901,7 +902,10 @@ def muon_step(params, grads, moms, *, lr, momentum=0.95, nesterov=True, weight_d
 
     params, grads (one dtype, bf16 or fp32) and moms (fp32) are tensors or lists as orthogonalize takes them.
     scale: a factor per entry of the list, one for all, or None: sqrt(max(1, cols / rows)), which for W [n_in,
-    n_out] layouts gives updates of the same effect whatever the shape."""
+    n_out] layouts gives updates of the same effect whatever the shape.
+    Matrices of one shape are best kept as one stack [count, rows, cols]: a call takes three launches for every 24
+    entries of the list whose short sides r have the same ceil(r / 16) (448 matrices of rank 16: 240 us in five
+    stacks, 1250 us one by one).  |a|^steps is limited as in orthogonalize."""
     P = _stacks("params", params)
     if not P:
         return

@@ -1622,8 +1622,9 @@ __global__ __launch_bounds__(NTH8, 1) void gemm_kernel(const GemmArgs args) {
   // instead of multiplying by zeros keeps an adapter that holds infinities to
   // its own rows, and costs eight vector instructions per two MFMAs in the
   // blocks concerned.  The sums reach the epilogue unrounded.
-  // Measured: 8192 x 4096 x 4096 with 16 adapters of rank 16 in runs of rows 203
-  // us, 1.36 PFLOP/s; 777 x 14336 x 4096, K in four ranges, 12 adapters of rank 64: 92 us.
+  // Measured (median, minimum): 8192 x 4096 x 4096 with 16 adapters of rank 16 in runs of rows 228, 197
+  // us, 1.2 to 1.4 PFLOP/s; 777 x 14336 x 4096, K in four ranges, 12 adapters of rank 64: 102, 94 us.
+  // Two parts of U against one: 1% with rows in runs, 3 to 8% where every tile meets 12 to 60 adapters.
   if constexpr (MULTI) {
     if (args.mt_plan != nullptr && kp <= 0) {
       const MultiTile& T = args.mt_plan[tm];

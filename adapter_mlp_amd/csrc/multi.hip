@@ -486,7 +486,7 @@ __global__ __launch_bounds__(256) void multi_shrink_kernel(const MultiArgs a) {
 // Four rows a block: lane 8 k +
 // j of a wavefront adds columns 8 j .. 8 j + 7 over every eighth K range from k,
 // and the eight sums of a column meet by a butterfly, so that the loads of 56
-// ranges (K = 14336) are two round trips.  5 to 7 us at both sizes above.
+// ranges (K = 14336) are two round trips.  6 to 7 us at both sizes above.
 __global__ __launch_bounds__(256) void multi_u_kernel(const MultiArgs a) {
   constexpr int AHEAD = 4;  // ranges a lane loads together (past the last one it is read again)
   const int lane = threadIdx.x & 63;
@@ -874,6 +874,7 @@ __global__ __launch_bounds__(256) void multi_f32_kernel(const MultiArgs a) {
 //    1472 x 704, 2 of rank 16: 25 / 45 at 1536;  60 of rank 64: 69 / 64
 //    14336 x 4096, 2 of rank 16: 79 / 90 at 300, 125 / 97 at 562
 //    128 x 1664, 2 of rank 16: 23 / 25 at 1536, 32 / 25 at 2304
+// (the many side with U in one bf16 part; two add 1 to 4% to it)
 // Up to kFewRows rows always few, past kManyRows always many.
 constexpr int64_t kFewRows = 128, kManyRows = 4096;
 int shrink_share(int64_t n);

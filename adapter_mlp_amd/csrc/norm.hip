@@ -130,7 +130,7 @@ constexpr bool norm_keep(bool bwd) {
 // Thread tx of a row's TPR threads owns the vectors tx, tx + TPR, ... (NV of
 // them) in every row it meets.
 // Measured: 8192 bf16 rows of 4096 with post-norm, column gate and pre-norm,
-// 268 MB: 46 us, 5.8 TB/s (a large copy: 4.85 TB/s, half of it written here as
+// 268 MB: 44 to 47 us, 5.7 to 6.1 TB/s (a large copy: 4.85 TB/s, half of it written here as
 // there; operands that were just read or written partly come from the last-level
 // cache).  One row of 4096: 3 us, the round trips of its loads and one sum.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
@@ -251,8 +251,10 @@ __global__ __launch_bounds__(norm_block<TPR>()) void norm_fwd_kernel(const NormA
 // registers of the thread that owns the column, one slice per block, and
 // norm_grad_kernel adds the slices in ascending order.
 // Measured: 8192 bf16 rows of 4096 with all three gradients, 403 MB and 25 MB of
-// slices: 81 us, 5.3 TB/s, and 5.5 us to add the slices.  1003 fp32 rows of 1001
-// (no 16-byte access, a row of 1001 at odd addresses): 12.8 + 3.9 us.
+// slices: 80 us, 5.3 TB/s, and 5.8 us to add the slices.  1003 fp32 rows of 1001:
+// 11.9 + 3.9 us for 24 MB, 2 TB/s.  Rows whose length is no multiple of four are
+// loaded element by element (VEC = 1), and one wavefront a row makes 251 blocks
+// of these, one wavefront a SIMD: too few loads in flight.
 template <typename TA, typename TP, int VEC, int TPR, int NV>
 __global__ __launch_bounds__(norm_block<TPR>(), TPR <= 256 ? 2 : 1) void norm_bwd_kernel(const NormArgs a) {
   constexpr bool PREFETCH = norm_prefetch<TA, VEC, TPR, NV>(true), KEEP = norm_keep<TA, VEC, TPR, NV>(true);
@@ -498,8 +500,12 @@ hipError_t launch_vec(const NormArgs& a, hipStream_t st) {
     if (a.H <= 6144) return launch_cfg<BWD, TA, TP, VEC, 768, 8>(a, st);
   }
   if (a.H <= 8192) return launch_cfg<BWD, TA, TP, VEC, 512, 16>(a, st);
-  // a bf16 backward's sums spill less from 512 threads of 32 elements than from 1024 of 16, which
-  // have 128 registers each (250 against 336 us at 2048 rows of 16384)
+  // A backward pass of wider rows holds three column sums beside five operands, which spill: a bf16 one
+  // less from 512 threads of 32 elements than from 1024 of 16, which have 128 registers each (250 against
+  // 336 us at 2048 rows of 16384).  Registers spilled a thread, and time at 2048 rows of 16384 with all
+  // gradients: bf16 139, 250 us (1.6 TB/s); bf16 with fp32 parameters 557, 503 us (0.8); fp32 314, 831 us
+  // (1.0); element by element 244 (655 us at 9001 columns, 0.7 TB/s), and from 4097 columns on 204 (245 us
+  // at 5001, 1.0 TB/s).  Up to 8192 columns the vector forms spill 8 registers at most and keep 3.3 TB/s.
   if constexpr (BWD && VEC == 8) return launch_cfg<BWD, TA, TP, VEC, 512, 32>(a, st);
   else return launch_cfg<BWD, TA, TP, VEC, 1024, 16>(a, st);
 }

@@ -360,10 +360,11 @@ __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_gram_kernel(const O
 // wavefront, so that the four matrix cores share each product evenly and one
 // wavefront's LDS reads hide behind another's MFMAs.  Rows are 16 NT + 2
 // doubles apart, which spreads the 16 rows of a fragment read over all banks.
-// Measured: 5 steps 46 to 52 us at rank 64 (6.5 a step, 4.7 of it the matrix
-// cores; the rest is the chunks' sum, 20 KB each into one CU, and the way in and
-// out), 9 us at rank 16 (0.9 a step, a chain of products), whatever the number
-// of matrices up to the chip's CUs.
+// Measured: 5 steps 46 to 53 us at rank 64, 33 of them the steps (6.5 each, 4.7 of
+// it the matrix cores, which are busy 29% of the kernel on the CUs that have a
+// matrix) and up to 20 the way in and out: one block sums the chunks of its matrix,
+// 20 KB each, 1.1 MB for a long side of 14336.  9.6 us at rank 16 (0.9 a step, a
+// chain of products), whatever the number of matrices up to the chip's CUs.
 // fp32 products would halve the steps and lose the small singular values: an error
 // of 2^-24 |G| in a direction of G's null space grows by a^2 a step.  In fp64 it is
 // 2^-53 |G|, and kMaxGrowth keeps it small.
@@ -498,7 +499,8 @@ __global__ __launch_bounds__(NT >= 3 ? 1024 : 256 * NT) void orth_steps_kernel(c
 // read back as it lies in memory for the update of P (loaded with U).
 // Measured: the update of 448 rank-16 matrices, 671 MB: 130 us, 5.2 TB/s, the
 // bound.  14 rank-64 matrices, 84 MB: 35 us, of which the full products in fp64
-// (16 tiles a sub-tile) take 13.
+// (16 tiles a sub-tile) take 13.  At NT = 4 the momentum forms spill 16 to 21 of 256
+// registers (P, U and the sums of a sub-tile at once).
 template <typename T, int NT, int MODE>
 __global__ __launch_bounds__(256, NT <= 2 ? 3 : 2) void orth_apply_kernel(const OrthArgs a) {
   constexpr int N = 16 * NT, LD = N + 2, S = N / 4;

@@ -417,7 +417,10 @@ lora_status lora_multi_workspace_size(const lora_multi_desc* desc, size_t* bytes
  * adapter.  W NULL: the adapter terms are added to what Y holds (the product
  * with a base kept in another form, e.g. lora_nf4_gemm's).  Each adapter, W,
  * X and Y must be smaller than 2 GiB - 4 KiB; the stacks may be larger.  No
- * output may overlap an input (LORA_EUNSUPPORTED). */
+ * output may overlap an input (LORA_EUNSUPPORTED).  The sums are fp32; in bf16
+ * s_i X[t] A[i] is kept to 2^-16 of itself at least, and Y rounded once.
+ * Adapters have the type of X: those of the fp32 LoRA-gradient mode are cast by
+ * the caller. */
 lora_status lora_multi_fwd(const lora_multi_desc* desc, const void* X, const void* W, const void* A, const void* B,
                            const float* scales, const int32_t* ids, void* Y, void* ws, size_t ws_bytes, void* stream);
 
@@ -439,7 +442,8 @@ typedef enum lora_gate {
  * LORA_BF16_F32LORA: bf16 activations, fp32 parameters (w_post, w_pre, a
  * column gate) and parameter gradients.  H is at most 16384, a positive
  * multiple of 64 in the bf16 modes; T is any count, and [T, H] tensors may
- * exceed 2 GiB.  All arithmetic is fp32; each output is rounded once. */
+ * exceed 2 GiB.  All arithmetic is fp32; each output is rounded once.  The sum
+ * of squares of a normed row has to lie in fp32's range. */
 typedef struct lora_norm_desc {
   int64_t T;            /* rows */
   int64_t H;            /* width of a row */
@@ -492,7 +496,9 @@ lora_status lora_block_norm_bwd(const lora_norm_desc* desc, const void* dR_out, 
  * adapters A [n_in, r] or B [r, n_out] of several layers or users.  G and P
  * have the descriptor's dtype (LORA_F32 or LORA_BF16), aligned to it.  A stack
  * holds fewer than 2^22 - 1 matrices, and fewer than 2^30 rows of the short
- * side's width in all; tensors may exceed 2 GiB. */
+ * side's width in all; tensors may exceed 2 GiB.  A call takes three launches,
+ * one after the other, for every 24 stacks whose short sides have the same
+ * ceil(r / 16): matrices of one shape are best given as one stack. */
 typedef struct lora_orth_mat {
   const void* G;   /* gradient (read) */
   float* M;        /* lora_muon_step: momentum, fp32 (updated); else NULL */
@@ -534,7 +540,8 @@ lora_status lora_orthogonalize(const lora_orth_desc* desc, const lora_orth_mat* 
 
 /* One optimizer step of every stack:
  *   M <- momentum M + G;  U = G + momentum M (nesterov) or M   (fp32)
- *   P <- (1 - lr weight_decay) P - lr scale NS(U)   (from the fp32 NS(U) in fp64)
+ *   P <- (1 - lr weight_decay) P - lr scale NS(U)   (from the fp32 NS(U) in fp64, rounded
+ *                                                    to fp32 and then to the type)
  * No tensor may overlap another (LORA_EUNSUPPORTED). */
 lora_status lora_muon_step(const lora_muon_desc* desc, const lora_orth_mat* mats, void* ws, size_t ws_bytes,
                            void* stream);
