@@ -298,28 +298,47 @@ def test_f32_at_four_byte_addresses(T, K, N, r):
     assert torch.equal(run(q, Y=shifted(torch.zeros(T, N, device="cuda"))), want)
 
 
-@pytest.mark.gpu
-@pytest.mark.parametrize("r", [16, 40])
-def test_split_and_unsplit_tiles_in_one_launch(r):
-    """272 tiles of 256 x 256 on 256 CUs: the last 16 are split over K, and take their adapters in the first part."""
-    T, K, N, n = 4349, 8192, 4096, 5
-    g = torch.Generator(device="cuda").manual_seed(r)
+def on_device(T, K, N, r, n, seed, dtype="bf16"):
+    g = torch.Generator(device="cuda").manual_seed(seed)
 
     def rnd(*shape, scale=1.0):
-        return (torch.randn(shape, generator=g, device="cuda") * scale).to(torch.bfloat16)
+        return (torch.randn(shape, generator=g, device="cuda") * scale).to(DT[dtype])
 
-    s = dict(X=rnd(T, K), W=rnd(K, N, scale=K ** -0.5), ids=torch.randint(-1, n, (T,), generator=g, device="cuda", dtype=torch.int32))
-    p = s["pool"] = lm.AdapterPool(A=rnd(n, K, r, scale=K ** -0.5), B=rnd(n, r, N, scale=r ** -0.5),
-                                   scale=torch.rand(n, generator=g, device="cuda") + 0.5)
-    X, W, c = s["X"].double(), s["W"].double(), (K / 32 + 16) * 2.0 ** -24
+    return dict(X=rnd(T, K), W=rnd(K, N, scale=K ** -0.5), ids=torch.randint(-1, n, (T,), generator=g, device="cuda", dtype=torch.int32),
+                pool=lm.AdapterPool(A=rnd(n, K, r, scale=K ** -0.5), B=rnd(n, r, N, scale=r ** -0.5),
+                                    scale=torch.rand(n, generator=g, device="cuda") + 0.5))
+
+
+def check_on_device(s):
+    """The call against float64 on the GPU, for sizes that take the CPU long; U to two bf16 parts."""
+    K, low, p = s["X"].shape[1], s["X"].dtype == torch.bfloat16, s["pool"]
+    n, _, r = p.A.shape
+    X, W, c = s["X"].double(), s["W"].double(), (K / 32 + 16 if low else K) * 2.0 ** -24
     y, mag = X @ W, c * (X.abs() @ W.abs())
+    del W
     for i in range(n):
         rows = torch.nonzero(s["ids"] == i).flatten()
         A, B, k = p.A[i].double(), p.B[i].double(), float(p.scale[i])
         U = X[rows] @ A
         y[rows] += k * (U @ B)
-        mag[rows] += k * ((c * (X[rows].abs() @ A.abs()) + (2.0 ** -16 + (r + 2) * 2.0 ** -24) * U.abs()) @ B.abs())
-    check(run(s), (y.cpu(), (HALF[torch.bfloat16] * y.abs() * (1 + 2.0 ** -7) + mag).cpu()))
+        mag[rows] += k * ((c * (X[rows].abs() @ A.abs()) + ((2.0 ** -16 if low else 0) + (r + 2) * 2.0 ** -24) * U.abs()) @ B.abs())
+    err = (run(s).double() - y).abs_()
+    bad = ~(err <= HALF[s["X"].dtype] * y.abs() * (1 + 2.0 ** -7) + mag)
+    assert not bad.any(), f"off by {err[bad].max():.3g} at {int(bad.sum())} of {err.numel()}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [16, 40])
+def test_split_and_unsplit_tiles_in_one_launch(r):
+    """272 tiles of 256 x 256 on 256 CUs: the last 16 are split over K, and take their adapters in the first part."""
+    check_on_device(on_device(4349, 8192, 4096, r, 5, seed=r))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,K,N,r,dtype", [(3, 1 << 22, 64, 8, "bf16"), (255, 1 << 22, 64, 16, "bf16"), (3, 64, 1 << 22, 64, "bf16"),
+                                           (255, 64, 1 << 22, 24, "bf16"), (3, 1 << 22, 33, 9, "f32"), (5, 33, 1 << 22, 64, "f32")])
+def test_widest_sides(T, K, N, r, dtype):
+    check_on_device(on_device(T, K, N, r, 3, 7, dtype))
 
 
 @pytest.mark.gpu
