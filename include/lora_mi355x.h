@@ -340,8 +340,8 @@ lora_status lora_moe_workspace_size(const lora_moe_desc* desc, size_t* bytes);
  *          w down_e (phi(gate_e X[t]) * (up_e X[t]))
  * router [E, H], gate and up [E + shared, I, H], down [E + shared, H, I]: every
  * expert's weights are stored [n_out, n_in] (as lora_proj.Wt), shared experts
- * last.  Logits are summed in fp64, products in fp32, in whose range gate_e X,
- * up_e X and h = phi * up have to lie; in bf16 h is kept to 2^-16 of itself and Y
+ * last.  Logits are products and sums in fp64, all other products fp32, in whose
+ * range gate_e X, up_e X and h = phi * up have to lie; in bf16 h is kept to 2^-16 of itself and Y
  * rounded once.  How sums are split depends on the sizes of the call, T among
  * them.  Experts that no token chose are not read.  Y may not overlap an input
  * (LORA_EUNSUPPORTED); X and the experts' h, [T (top_k + shared), I] of 4 bytes,

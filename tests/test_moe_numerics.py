@@ -1,0 +1,63 @@
+"""moe_fwd where its numbers go to their ends.  References and bounds: _moe_ref.py."""
+import pytest
+import torch
+
+from _moe_ref import check_rows, routing
+from test_moe import make, run
+
+
+def choices(T, H, E, mode, *, shifted=False, seed=0, device="cuda"):
+    """A layer of top-1 experts that differ, and X, router whose best two logits of every token lie 1e-11 to 1e-8 apart:
+    experts 2 i and 2 i + 1 have the same row but for one element, moved by a step of its type."""
+    s = make(T, H, 64, E, 1, mode, seed=seed, device=device)
+    r = s["ex"].router
+    r[1::2] = r[0:E // 2 * 2:2]
+    j = torch.arange(E // 2, device=device) * 7 % H
+    i = torch.arange(E // 2, device=device)
+    step = 2.0 ** -7 if r.dtype == torch.bfloat16 else 2.0 ** -23
+    old = r[2 * i, j].float()
+    old = torch.where(old.abs() < 0.02, torch.full_like(old, 0.02), old).to(r.dtype)
+    r[2 * i, j] = old
+    r[2 * i + 1, j] = (old.double() * (1 + step)).to(r.dtype)
+    x = s["X"][:, j].double()
+    x = torch.where(x < 0, x - 0.5, x + 0.5)  # no gap of nothing
+    s["X"][:, j] = (x * (2.0 ** -20 if r.dtype == torch.bfloat16 else 2.0 ** -6)).to(s["X"].dtype)
+    if shifted:
+        for name in ("X", "router"):
+            t = s["X"] if name == "X" else r
+            u = torch.empty(t.numel() + 1, dtype=t.dtype, device=device)[1:].view(t.shape).copy_(t)
+            if name == "X":
+                s["X"] = u
+            else:
+                s["ex"].router = u
+    return s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,E", [(1, 192, 16), (2, 512, 200), (4, 2048, 64), (30, 256, 16), (30, 256, 100), (200, 320, 400)])
+@pytest.mark.parametrize("mode", ["bf16", "bf16_f32", "f32", "f32 shifted"])
+def test_choice_between_near_logits(T, H, E, mode):
+    """Products of two bf16 or fp32 numbers are exact in fp64, so a logit is off by a few 2^-53 of its terms, and by nothing
+    of a sum's order or an address's alignment that could turn the choice."""
+    s = choices(T, H, E, mode.split()[0], shifted=mode.endswith("shifted"), seed=T)
+    l = (s["X"].double().cpu() @ s["ex"].router.double().cpu().t())
+    top = l.topk(2, dim=1).values
+    gap = top[:, 0] - top[:, 1]
+    assert (gap > 1e-11).all() and (gap < 1e-8).all()
+    assert torch.equal(routing(s)[0][:, 0].cpu(), l.argmax(1))
+    check_rows(s, run(s))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E", [4, 200])
+@pytest.mark.parametrize("T", [1, 3, 50])
+@pytest.mark.parametrize("mode", ["bf16", "bf16_f32", "f32"])
+def test_choice_after_cancellation(T, E, mode):
+    """Logits of 1 and 1/2 that are left of terms of 2^24."""
+    s = make(T, 64, 64, E, 1, mode)
+    s["X"][:, :3] = torch.tensor([4096.0, 1.0, 4096.0])
+    s["ex"].router.zero_()
+    s["ex"].router[1, :3] = torch.tensor([0.0, 0.5, 0.0])
+    s["ex"].router[2, :3] = torch.tensor([4096.0, 1.0, -4096.0])
+    assert (routing(s)[0] == 2).all()
+    check_rows(s, run(s))
