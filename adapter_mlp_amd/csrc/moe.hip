@@ -66,7 +66,7 @@ struct MoeArgs {
 // tokens: 8.0 against 5.1).  The choice of experts hangs on the last bits of near ties, so
 // products, which fp64 holds exactly for bf16 and fp32 inputs, and sums are fp64: off by a
 // few 2^-53 of the terms, whichever lanes they fall to.  (Runs of V products in fp32, added up in fp64:
-// 1 us less at 64 to 256 tokens on up to 128 experts, 8 of 327 us a call at 200 on 256 of 4096 x 256.)
+// 1 to 2 us less at 64 to 256 tokens on 64 to 128 experts, 8 of 327 us a call at 200 on 256 of 4096 x 256.)
 // ---------------------------------------------------------------------------
 template <typename TX, typename TR, int V, int TW, int KW>
 __global__ __launch_bounds__(256) void moe_logits_kernel(const MoeArgs a) {
@@ -116,6 +116,18 @@ __device__ __forceinline__ uint64_t order_key(double x) {
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
 
+// A sigmoid over exp(m), m = min(0, the largest logit that a token chose) where its weights are normalised, else 0:
+// with 1 for the largest of small scores the quotient is what it is however far down the logits lie (in fp32, and
+// undivided, scores were subnormal from logits of -88 on and all 0 from -104 on).
+__device__ __forceinline__ double sigmoid_over(double l, double m) {
+  return l > 0.0 ? 1.0 / (1.0 + exp(-l)) : exp(l - m) / (1.0 + exp(l));
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) x += __shfl_xor(x, d);
+  return x;
+}
+
 __device__ __forceinline__ void choose(const MoeArgs& a, int t, const double* l) {
   __shared__ uint64_t key[kMaxE];
   __shared__ int place[kMaxE];
@@ -151,19 +163,30 @@ __device__ __forceinline__ void choose(const MoeArgs& a, int t, const double* l)
   __syncthreads();
   if (tid >= 64) return;
   const bool routed = tid < a.k;
-  const double x = routed ? chosen_l[tid] : 0.0, top = chosen_l[0];
-  const float w = !routed ? 0.0f : sig ? (float)(1.0 / (1.0 + exp(-x))) : expf((float)(x - top));
-  float sum = w;
-  if (!a.normalize && !sig) {
-    sum = 0.0f;
-    for (int i = tid; i < a.E; i += 64) sum += expf((float)(l[i] - top));
-  }
+  float w;  // sigmoids and their quotient are fp64, rounded once
+  if (sig) {
+    double m = routed && a.normalize ? chosen_l[tid] : -INFINITY;
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    for (int d = 32; d > 0; d >>= 1) m = fmax(m, __shfl_xor(m, d));
+    const double s = routed ? sigmoid_over(chosen_l[tid], a.normalize ? fmin(m, 0.0) : 0.0) : 0.0;
+    const double sum = a.normalize ? wave_sum(s) : 1.0;
+    w = (float)(s / sum * (double)a.scale);
+  } else {
+    const double top = chosen_l[0];
+    w = routed ? expf((float)(chosen_l[tid] - top)) : 0.0f;
+    float sum = w;
+    if (!a.normalize) {
+      sum = 0.0f;
+      for (int i = tid; i < a.E; i += 64) sum += expf((float)(l[i] - top));
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+    w = w / sum * a.scale;
+  }
   if (tid < a.kk) {
     a.ids[t * a.kk + tid] = routed ? chosen[tid] : a.E + tid - a.k;
     if (routed) a.place[chosen[tid] * a.Tp + t] = (uint8_t)(tid + 1);
-    a.w[t * a.kk + tid] = routed ? (a.normalize || !sig ? w / sum * a.scale : w * a.scale) : 1.0f;
+    a.w[t * a.kk + tid] = routed ? w : 1.0f;
   }
 }
 __global__ __launch_bounds__(kMaxE) void moe_select_kernel(const MoeArgs a) {
@@ -878,19 +901,34 @@ __device__ __forceinline__ int choose_one(const MoeArgs& a, int (*part)[128], in
     const uint64_t m = __ballot(place[0] == 0);
     const int at = __builtin_ctzll(m ? m : __ballot(place[1] == 0));
     const double top = __shfl(m ? l[0] : l[1], at);
-    float w[2], sum = 0.0f;
+    float w[2];
+    if (sig) {
+      double s[2], sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      w[i] = sig ? (float)(1.0 / (1.0 + exp(-l[i]))) : expf((float)(l[i] - top));
-      if (place[i] < (a.normalize ? a.k : a.E)) sum += w[i];
+      for (int i = 0; i < 2; ++i) {
+        s[i] = sigmoid_over(l[i], a.normalize ? fmin(top, 0.0) : 0.0);
+        if (place[i] < a.k) sum += s[i];
+      }
+      sum = a.normalize ? wave_sum(sum) : 1.0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = (float)(s[i] / sum * (double)a.scale);
+    } else {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        w[i] = expf((float)(l[i] - top));
+        if (place[i] < (a.normalize ? a.k : a.E)) sum += w[i];
+      }
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) w[i] = w[i] / sum * a.scale;
     }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       if (place[i] < a.k) {
         a.ids[place[i]] = 64 * i + lane;
-        a.w[place[i]] = a.normalize || !sig ? w[i] / sum * a.scale : w[i] * a.scale;
+        a.w[place[i]] = w[i];
       }
     if (lane < a.shared) {
       a.ids[a.k + lane] = a.E + lane;

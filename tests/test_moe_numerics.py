@@ -61,3 +61,33 @@ def test_choice_after_cancellation(T, E, mode):
     s["ex"].router[2, :3] = torch.tensor([4096.0, 1.0, -4096.0])
     assert (routing(s)[0] == 2).all()
     check_rows(s, run(s))
+
+
+# T, E: one token whose choice is made beside gate and up; a small router; the choice as a launch of its own; many tokens
+ROUTES = [(1, 16), (1, 300), (5, 16), (6, 400), (40, 16), (70, 500)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("level", [-20.0, -87.0, -95.0, -103.0, -110.0, -700.0, -744.0, -1000.0, -30000.0])
+@pytest.mark.parametrize("mode", ["bf16", "f32"])
+@pytest.mark.parametrize("T,E", ROUTES)
+def test_sigmoid_weights_of_far_logits(T, E, mode, level):
+    """Normalised, they are those of the quotient, finite however small the scores are."""
+    for k, bias in ((3, False), (1, False), (3, True)):
+        s = make(T, 192, 64, E, k, mode, score="sigmoid", bias=bias, scale=1.5, shared=1, seed=T + E)
+        s["X"][:, 0] = 1.0
+        s["ex"].router[:, 0] = level
+        ids, w = routing(s)
+        assert w.isfinite().all() and torch.allclose(w.sum(1), torch.full_like(w[:, 0], 1.5))
+        check_rows(s, run(s))
+    # one chosen logit far above the others: no score is lost either way
+    s = make(T, 192, 64, E, 3, mode, score="sigmoid", seed=1)
+    s["X"][:, 0] = 1.0
+    s["ex"].router[:, 0] = level
+    s["ex"].router[E // 2, 0] = 5.0
+    check_rows(s, run(s))
+    # without the quotient the scores themselves, which may be nothing in Y's type
+    s = make(T, 192, 64, E, 3, mode, score="sigmoid", normalize=False, shared=1, seed=2)
+    s["X"][:, 0] = 1.0
+    s["ex"].router[:, 0] = level
+    check_rows(s, run(s))
