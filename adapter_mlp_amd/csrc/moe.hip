@@ -567,15 +567,19 @@ __device__ __forceinline__ void store_h(const MoeArgs& a, int slot, int64_t n, f
   if constexpr (sizeof(T) == 2) {
     // Two bf16 parts keep 2^-16 of h, so that Y is rounded once in effect.  The high one is cut off and
     // the low one rounded, so that both have h's sign and an infinity in down is multiplied into the
-    // same infinity twice; a low part of zero, which would give NaN there, is the smallest normal number
-    // instead, 2^-16 of h at most.
+    // same infinity twice.  That asks for a low part that is a normal number and not zero: where it
+    // would be less, the high part goes down a step, which the low one then holds (2^-15 of h is kept where that
+    // is below 2^-110); below 2^-118, where a step is less than the smallest normal number, it goes
+    // down by that number (h is kept to 2^-134).  h below 2^-125 has no two such parts; its low one may be zero.
     uint32_t hi[4];
     float lo[4];
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      hi[v] = __float_as_uint(h[v]) & 0xffff0000u;
-      const float d = h[v] - __uint_as_float(hi[v]);
-      lo[v] = d == 0.0f && fabsf(h[v]) >= 0x1p-110f ? copysignf(0x1p-126f, h[v]) : d;
+      const uint32_t bits = __float_as_uint(h[v]);
+      hi[v] = bits & 0xffff0000u;
+      if (fabsf(h[v] - __uint_as_float(hi[v])) < 0x1p-126f && fabsf(h[v]) >= 0x1p-125f)
+        hi[v] = fabsf(h[v]) >= 0x1p-118f ? hi[v] - 0x10000u : __float_as_uint(h[v] - copysignf(0x1p-126f, h[v])) & 0xffff0000u;
+      lo[v] = h[v] - __uint_as_float(hi[v]);
       if (!__builtin_isfinite(h[v])) {
         hi[v] = f2bf(h[v]) << 16;
         lo[v] = h[v];

@@ -91,3 +91,36 @@ def test_sigmoid_weights_of_far_logits(T, E, mode, level):
     s["X"][:, 0] = 1.0
     s["ex"].router[:, 0] = level
     check_rows(s, run(s))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 3, 30])
+@pytest.mark.parametrize("m", [1.0, 1.0078125])
+def test_small_hidden_values(T, mode, m):
+    """h of 2^-125 and more keeps its value, and an infinity in down stays one of its sign.  h is m^2 2^-p for ever larger p,
+    an expert a p: its parts, where it is kept in two, end below the normal numbers."""
+    ps = [0, 60, 95, 100, 103, 104, 108, 109, 110, 111, 112, 115, 116, 117, 118, 119, 120, 122, 123, 124, 125]
+    for p in ps:
+        for sign in (1.0, -1.0):
+            s = make(T, 128, 64, 4, 2, mode, shared=1)
+            for name in ("gate", "up", "down"):
+                getattr(s["ex"], name).zero_()
+            s["X"][:, 0] = 1.0
+            # phi(x) of a small x is x / 2, of a large one x
+            big = p == 0
+            s["ex"].gate[4, 7, 0] = 64.0 * m if big else m * 2.0 ** -(p // 2)
+            s["ex"].up[4, 7, 0] = sign * m * 2.0 ** -(p - p // 2 - (0 if big else 1))
+            s["ex"].down[4, 3, 7] = float("inf")
+            s["ex"].down[4, 5, 7] = float("-inf")
+            s["ex"].down[4, 9, 7] = 1.5 * 2.0 ** (p // 2)
+            y = run(s).double()
+            assert (y[:, 3] == sign * float("inf")).all() and (y[:, 5] == -sign * float("inf")).all(), p
+            x = m * 2.0 ** -(p // 2)
+            h = (64.0 * m if big else x / (1 + torch.tensor(-x, dtype=torch.float64).exp())) * m * 2.0 ** -(p - p // 2 - (0 if big else 1))
+            want = sign * h * 1.5 * 2.0 ** (p // 2)
+            # half a step of Y's type, 2^-16 of h (two steps of 2^-133 at its smallest), phi's 16 * 2^-24 and two more roundings
+            tol = (2.0 ** -8 + max(2.0 ** -16, 2.0 ** (p - 134)) if mode == "bf16" else 2.0 ** -24) + 18 * 2.0 ** -24
+            assert ((y[:, 9] - want).abs() <= tol * abs(want)).all(), (p, float(y[0, 9]), float(want))
+            keep = [n for n in range(128) if n not in (3, 5, 9)]
+            assert not y[:, keep].any()
