@@ -527,11 +527,31 @@ bool period_apart(const Ext& a, const Ext& b, int64_t Sa, int64_t span_a, int64_
   if (delta < 0) delta += Sa;
   return delta >= span_a && delta + span_b <= Sa;
 }
+// Rows that lie between each other's along both the tokens and the heads (q, k and v head by head,
+// [T, h, 3, d]).  With the same strides in both, rows (t, i) of a and (t', i') of b begin
+// a - b + (t - t') st + (i - i') sh apart, and meet where that is in (-a.d, b.d): for every i - i' the
+// t - t' that do so are a range.  A stride of a single token or head is the other's.
+bool lattice_apart(const Ext& a, const Ext& b) {
+  if ((a.T > 1 && b.T > 1 && a.st != b.st) || (a.h > 1 && b.h > 1 && a.sh != b.sh)) return false;
+  const int64_t st = a.T > 1 ? a.st : b.T > 1 ? b.st : 0, sh = a.h > 1 ? a.sh : b.h > 1 ? b.sh : 0;
+  const int64_t base = (int64_t)((intptr_t)a.p - (intptr_t)b.p);
+  for (int64_t i = 1 - b.h; i < a.h; ++i) {
+    const int64_t lo = -a.d - (base + i * sh), hi = b.d - (base + i * sh);  // of (t - t') st, both ends out
+    if (st == 0) {
+      if (lo < 0 && hi > 0) return false;
+      continue;
+    }
+    // floor(lo / st) + 1 .. ceil(hi / st) - 1
+    const int64_t first = (lo >= 0 ? lo / st : -((st - 1 - lo) / st)) + 1, last = (hi > 0 ? (hi - 1) / st : -((st - hi) / st));
+    if (std::max(first, 1 - b.T) <= std::min(last, a.T - 1)) return false;
+  }
+  return true;
+}
 bool apart(const Ext& a, const Ext& b) {
   if (a.p == nullptr || b.p == nullptr || a.bytes() == 0 || b.bytes() == 0) return true;
   if (!overlaps(a.p, (size_t)a.bytes(), b.p, (size_t)b.bytes())) return true;
   return (a.st > 0 && period_apart(a, b, a.st, (a.h - 1) * a.sh + a.d, b.st, (b.h - 1) * b.sh + b.d)) ||
-         (a.sh > 0 && period_apart(a, b, a.sh, (a.T - 1) * a.st + a.d, b.sh, (b.T - 1) * b.st + b.d));
+         (a.sh > 0 && period_apart(a, b, a.sh, (a.T - 1) * a.st + a.d, b.sh, (b.T - 1) * b.st + b.d)) || lattice_apart(a, b);
 }
 bool same(const Ext& a, const Ext& b) {
   return a.p == b.p && a.T == b.T && a.h == b.h && a.d == b.d && (a.T <= 1 || a.st == b.st) && (a.h <= 1 || a.sh == b.sh);
@@ -559,7 +579,7 @@ lora_status check_heads(const lora_rope_desc* d, const RopeSizes& z, const lora_
 lora_status check_overlap(const Ext* in, const int* in_kin, int ni, const Ext* out, const int* out_kin, int no) {
   for (int i = 0; i < no; ++i) {
     for (int j = 0; j < ni; ++j)
-      CHECK(apart(out[i], in[j]) || (in_kin[j] >= 0 && in_kin[j] == out_kin[i] && same(out[i], in[j])), LORA_EUNSUPPORTED,
+      CHECK((in_kin[j] >= 0 && in_kin[j] == out_kin[i] && same(out[i], in[j])) || apart(out[i], in[j]), LORA_EUNSUPPORTED,
             "%s overlaps %s", out[i].name, in[j].name);
     for (int j = 0; j < i; ++j)
       CHECK(apart(out[i], out[j]), LORA_EUNSUPPORTED, "%s overlaps %s", out[i].name, out[j].name);

@@ -581,7 +581,9 @@ lora_status lora_qk_norm_rope_workspace_size(const lora_rope_desc* desc, size_t*
  * axis NULL: axis 0 (axes must be 1); a pair whose axis lies outside [0, axes)
  * has a = 0.  An output may be exactly its input (same address and strides); it
  * shares memory with nothing else (LORA_EUNSUPPORTED), where parts of one
- * buffer, as Q and K of a fused buffer, are apart. */
+ * buffer whose rows do not meet, as Q and K of a fused buffer [T, heads, d] or
+ * [T, heads, 3, d], are apart; this is found for tensors that take turns along
+ * their tokens or heads and for those of the same strides. */
 lora_status lora_qk_norm_rope_fwd(const lora_rope_desc* desc, const lora_heads* Q, const lora_heads* K,
                                   const int32_t* pos, const float* inv_freq, const int32_t* axis, const void* w_q,
                                   const void* w_k, const lora_heads* Q_out, const lora_heads* K_out, void* stream);
