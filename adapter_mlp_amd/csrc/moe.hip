@@ -194,10 +194,12 @@ __global__ __launch_bounds__(kMaxE) void moe_select_kernel(const MoeArgs a) {
 }
 
 // Logits and choice of a token in one block, where the router is small and a launch costs more
-// than every block's reading of it: a wavefront has four experts at a time.  (17 tokens, fp32 router of
-// 10 x 250: 20.5 against 21.8 us a call on the GPU; 160 tokens, 32 x 1024 in bf16, 27.2 against 28.5; 40 tokens, 100 x 1024, 35.7
-// against 32.7.)
+// than every block's reading of it: a wavefront has four experts at a time, so 32 of them are a round trip.
+// (GPU us a call, against two launches: 17 tokens, fp32 router of 10 x 250: 16.5 and 17.7; 160 tokens, 32 x 1024 in bf16,
+// 33.9 and 35.6; 40 tokens, 100 x 1024, 61.4 and 59.2; 60 tokens in fp32, 64 x 128 17.5 and 18.7, 80 x 128 19.3 and 18.7,
+// 256 x 64 31.5 and 24.8; in bf16, 512 x 64 59.8 and 40.7.)
 constexpr int64_t kRouteBytes = 64 * 1024;
+constexpr int kRouteE = 64;
 template <typename TX, typename TR, int V>
 __global__ __launch_bounds__(kMaxE) void moe_route_kernel(const MoeArgs a) {
   constexpr int EW = 4, WAVES = kMaxE / 64;
@@ -1284,7 +1286,7 @@ lora_status lora_moe_fwd(const lora_moe_desc* d, const void* X, const void* rout
   // the router's 16-byte loads in fp32: whole vectors in every row, at aligned addresses
   const bool vx = d->H % 4 == 0 && aligned(X, 16) && aligned(router, 16);
   const bool one = bf16 && choose_in_up(a);
-  const bool route = !one && d->E * d->H * (int64_t)rs <= kRouteBytes;
+  const bool route = !one && d->E <= kRouteE && d->E * d->H * (int64_t)rs <= kRouteBytes;
   if (route) {
     if (d->dtype == LORA_BF16) LAUNCHN("moe_route", st, (launch_route<uint16_t, uint16_t, 8>(a, st)));
     else if (bf16) LAUNCHN("moe_route", st, (launch_route<uint16_t, float, 8>(a, st)));

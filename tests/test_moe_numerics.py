@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import adapter_mlp_amd as lm
 from _moe_ref import check_rows, routing
 from test_moe import make, run
 
@@ -124,3 +125,17 @@ def test_small_hidden_values(T, mode, m):
             assert ((y[:, 9] - want).abs() <= tol * abs(want)).all(), (p, float(y[0, 9]), float(want))
             keep = [n for n in range(128) if n not in (3, 5, 9)]
             assert not y[:, keep].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,H,mode,one", [(64, 512, "bf16", True), (64, 64, "f32", True), (65, 64, "f32", False), (512, 64, "bf16", False),
+                                          (8, 4096, "bf16", True), (8, 4160, "bf16", False)])
+def test_launches_of_the_choice(E, H, mode, one):
+    """Logits and choice in one launch only where every token's block is quick to read the whole router."""
+    s = make(20, H, 64, E, 2, mode)
+    lm.trace_begin("moe")
+    got = run(s)
+    torch.cuda.synchronize()
+    names = set(lm.trace_end())
+    assert names & {"moe_route", "moe_logits", "moe_select"} == ({"moe_route"} if one else {"moe_logits", "moe_select"})
+    check_rows(s, got)
