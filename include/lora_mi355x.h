@@ -343,10 +343,12 @@ lora_status lora_moe_workspace_size(const lora_moe_desc* desc, size_t* bytes);
  * last.  Logits are products and sums in fp64, all other products fp32, in whose
  * range gate_e X, up_e X and h = phi * up have to lie; a softmax is fp32, sigmoids
  * and their quotient are fp64, and w is fp32; in bf16 h is kept to 2^-16 of itself
- * (2^-15 below 2^-110, and never to less than 2^-134) and Y rounded once.  How sums are split depends on the sizes of the call, T among
- * them.  Experts that no token chose are not read.  Y may not overlap an input
- * (LORA_EUNSUPPORTED); X and the experts' h, [T (top_k + shared), I] of 4 bytes,
- * are smaller than 2 GiB - 4 KiB. */
+ * (2^-15 below 2^-110, and never to less than 2^-134) and Y rounded once.  How sums
+ * are split depends on the sizes of the call, T among them, and in fp32 of more
+ * than 16 tokens on how many of them chose an expert, so that there a token's last
+ * bits may differ with the others.  Experts that no token chose are not read.  Y
+ * may not overlap an input (LORA_EUNSUPPORTED); X and the experts' h,
+ * [T (top_k + shared), I] of 4 bytes, are smaller than 2 GiB - 4 KiB. */
 lora_status lora_moe_fwd(const lora_moe_desc* desc, const void* X, const void* router, const float* bias, const void* gate,
                          const void* up, const void* down, void* Y, void* ws, size_t ws_bytes, void* stream);
 

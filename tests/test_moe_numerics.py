@@ -139,3 +139,20 @@ def test_launches_of_the_choice(E, H, mode, one):
     names = set(lm.trace_end())
     assert names & {"moe_route", "moe_logits", "moe_select"} == ({"moe_route"} if one else {"moe_logits", "moe_select"})
     check_rows(s, got)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mode,T,H,I,E,k", [("bf16", 2, 192, 64, 6, 2), ("bf16", 8, 256, 192, 4, 2), ("bf16", 8, 256, 192, 200, 2),
+                                            ("bf16", 40, 256, 192, 4, 2), ("bf16", 200, 4096, 192, 6, 3), ("bf16", 256, 192, 1088, 40, 3),
+                                            ("f32", 9, 100, 70, 5, 2), ("f32", 16, 130, 200, 3, 3)])
+def test_a_token_does_not_hang_on_the_others(mode, T, H, I, E, k):
+    """In bf16, and in fp32 of up to 16 tokens, a token's bits are the same whatever the others choose."""
+    s = make(T, H, I, E, k, mode, shared=1)
+    want = run(s)
+    other = make(T, H, I, E, k, mode, shared=1, seed=1)["X"]
+    for t in (0, T - 1):
+        alike = dict(s, X=s["X"][t].expand(T, -1).contiguous())  # all on the same experts
+        assert torch.equal(run(alike), want[t].expand(T, -1))
+        mixed = other.clone()
+        mixed[t] = s["X"][t]
+        assert torch.equal(run(dict(s, X=mixed))[t], want[t])
