@@ -18,10 +18,10 @@
 // own in h and in the products of down.
 //
 // Measured, in bf16, all launches (a read-only stream reaches 7.2 TB/s on this
-// chip): 64 tokens, 8 of 128 experts of 2048 x 768: 205 us, 1.19 GB, of which gate / up
-// 122 us and down 66 us at 6.3 to 6.5 TB/s; 33 tokens, 2 of 8 of 4096 x 14336: 455 us, 2.8 GB,
-// 290 and 145 us, 6.5 TB/s; one token, 8 of 128: 25 us, 76 MB, three launches of which
-// none is long enough to reach the rate (2.6, 15 and 8 us).
+// chip): 64 tokens, 8 of 128 experts of 2048 x 768: 205 us, 1.22 GB, of which gate / up
+// 127 us and down 67 us at 6.3 TB/s; 33 tokens, 2 of 8 of 4096 x 14336: 458 us, 2.9 GB,
+// 301 and 146 us at 6.3 and 6.9 TB/s; one token, 8 of 128: 25 us, 76 MB, three launches of which
+// none is long enough to reach the rate (2.7, 16 and 8 us).
 #include <algorithm>
 #include <cmath>
 
@@ -62,8 +62,8 @@ struct MoeArgs {
 
 // ---------------------------------------------------------------------------
 // Logits: a wavefront has one expert and TW tokens, or where these are few
-// (KW = 4) the block's four take turns at the inputs (1 token: 2.6 against 3.3 us; 64
-// tokens: 8.0 against 5.1).  The choice of experts hangs on the last bits of near ties, so
+// (KW = 4) the block's four take turns at the inputs (calls on 128 experts of width 2048: 1 token 24.2 and without
+// 25.8 us, 64 tokens 200.4 and 198.2).  The choice of experts hangs on the last bits of near ties, so
 // products, which fp64 holds exactly for bf16 and fp32 inputs, and sums are fp64: off by a
 // few 2^-53 of the terms, whichever lanes they fall to.  (Runs of V products in fp32, added up in fp64:
 // 1 to 2 us less at 64 to 256 tokens on 64 to 128 experts, 8 of 327 us a call at 200 on 256 of 4096 x 256.)
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(const MoeArgs a) {
 // Choice, a block a token.  Order: the larger key, then the lower index; NaN
 // comes after every number.  An expert's place is the number of experts before
 // it, counted by all threads at once: E^2 comparisons, but no chain of
-// reductions.  (128 experts, 8 of them: 3.5 us, k rounds of a wavefront's argmax
+// reductions.  (128 experts, 8 of them: 4 to 4.8 us, k rounds of a wavefront's argmax
 // 9.4 us.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint64_t order_key(double x) {
@@ -872,9 +872,9 @@ __global__ __launch_bounds__(64 * NW, 2) void moe_ring_kernel(const MoeArgs a) {
 // The choice for one token of up to 128 experts (without a selection bias) by
 // every block of gate and up for itself, instead of a launch in between; the first
 // block leaves it for the later launch.  Each wavefront counts over a quarter
-// of the experts, two a lane.  Returns the expert of this block.  (8 of 128 experts of
-// 2048 x 768: 25.2 against 26.6 us a call, gate and up 15 against 3.4 + 12.1; 2 of 8 of
-// 512 x 256, where launches count: 17.5 against 20.8.)
+// of the experts, two a lane.  Returns the expert of this block.  (GPU us a call against
+// a launch for it: 8 of 128 experts of 2048 x 768 24.2 and 24.5, 8 + 2 of 64 of 1024 x 256 15.4 and 16.6, 2 of 8 of
+// 512 x 256 11.5 and 12.6, from Python 17.5 and 20.8.)
 __device__ __forceinline__ int choose_one(const MoeArgs& a, int (*part)[128], int unit, int wave, int lane) {
   const bool sig = a.score == LORA_SCORE_SIGMOID;
   double l[2];
